@@ -463,6 +463,143 @@ ADAFUSE_API int adafuse_segment_table(const adafuse_desc* desc, int32_t* entries
 ADAFUSE_API int adafuse_switch_noalloc(const adafuse_desc* desc, const adafuse_route* prev,
                                        const adafuse_route* cur, int32_t* status, void* stream);
 
+/* ---- per-token experts ----------------------------------------------------
+ * Tokens that cannot share one merged W -- a prompt, or a decode batch whose
+ * sequences each chose their own experts -- keep W as it is and add their own
+ * gated experts to its product (the unmerged forward of dynamic adapters,
+ * gist.science technical summary, section 1, which the merged form replaces
+ * for one decision per step).  Three calls: a router that makes one decision
+ * per token, the product of a weight with a fused epilogue, and the same
+ * product with every token's own experts.  All three read the context without
+ * changing it (device status word apart), so they may run on several streams
+ * at once, each with its own workspace, while no call that changes the
+ * context or its W is in flight. */
+
+#define ADAFUSE_DTYPE_BF16 0
+#define ADAFUSE_DTYPE_F32  1
+
+/* Eight-slot route record (64 bytes): as adafuse_route4 with eight slots.
+ * Read by adafuse_linear_routed only; the switches take 2 or 4 slots. */
+#define ADAFUSE_MAX_ROUTE_SLOTS 8
+typedef struct adafuse_route8 {
+    int32_t idx[8];
+    float gate[8];
+} adafuse_route8;
+
+#define ADAFUSE_SCORE_SOFTMAX 0  /* score_e = softmax over all E of the logits */
+#define ADAFUSE_SCORE_SIGMOID 1  /* score_e = 1 / (1 + exp(-z_e)) */
+
+/* How adafuse_route_experts decides (host memory, read during the call).
+ *   k           experts per token, 1..8 (at most `slots`).
+ *   n_groups    the E experts are n_groups equal runs (1 = no groups; divides
+ *               E).  Only experts of the top_groups best groups can be
+ *               picked; a group's worth is the sum of its group_top (1 or 2)
+ *               highest selection values, the lower group first among equals.
+ *   renorm      nonzero: a token's gates are divided by their sum.
+ *   scale       finite factor on every gate.
+ *   bias        device [E] fp32 or NULL: added to the score for selection,
+ *               never to the gate (a balance bias).  -infinity or NaN
+ *               disables the expert; +infinity picks it first. */
+typedef struct adafuse_gating {
+    int32_t score;
+    int32_t k;
+    int32_t n_groups;
+    int32_t top_groups;
+    int32_t group_top;
+    int32_t renorm;
+    float scale;
+    const float* bias;
+} adafuse_gating;
+
+/* One routing decision per token:
+ *   z_e = sum_i h[t,i] * Wr[i,e]
+ *   selection value  q_e = score_e + bias_e;  without a bias experts rank by
+ *         z_e (the score is increasing in it)
+ *   the k experts first under (selection descending, index ascending) inside
+ *         the kept groups; fewer than k enabled there leaves slots empty
+ *   gate_j = scale * score_j, or scale * score_j / sum of the picks' scores
+ * written to route[t], a record of `slots` (2, 4 or 8) slots: int32 idx[slots]
+ * then fp32 gate[slots], empty slots idx -1, gate 0 -- adafuse_route,
+ * adafuse_route4 or adafuse_route8.  Picks are those of the logits and scores
+ * in 64 bits: the kernel works in 32 bits with an error bound and settles in
+ * 64 what the bound leaves open.  Gates come from 32-bit logits.  A token with
+ * a logit that is not a finite fp32 number gets an empty record.
+ * h: [T, d] of h_dtype (ADAFUSE_DTYPE_*), rows ldh elements apart, 16-byte
+ * aligned, d and ldh multiples of 4, ldh >= d.  Wr: [d, E] fp32, 4-byte
+ * aligned.  route: 16-byte aligned.  E comes from the context.  T == 0 is a
+ * no-op.  One launch on `stream`. */
+ADAFUSE_API int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int64_t T,
+                                      int64_t d, int64_t ldh, const float* Wr,
+                                      const adafuse_gating* gating, int32_t slots, void* route,
+                                      void* stream);
+
+#define ADAFUSE_WEIGHT_CURRENT 0  /* W, with whatever the switches have merged into it */
+#define ADAFUSE_WEIGHT_BASE    1  /* the pristine copy registered by adafuse_set_base */
+
+#define ADAFUSE_ACT_NONE      0
+#define ADAFUSE_ACT_RELU      1
+#define ADAFUSE_ACT_GELU      2  /* v/2 * (1 + erf(v / sqrt 2)) */
+#define ADAFUSE_ACT_GELU_TANH 3  /* v/2 * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) */
+#define ADAFUSE_ACT_SILU      4  /* v / (1 + exp(-v)) */
+
+/* One product with a weight of the context (host memory, read during the call):
+ *   y = residual + mul * act(x W^T + bias)
+ *   x         [T, in] bf16, rows ldx elements apart.
+ *   bias      [out] fp32, 4-byte aligned, or NULL.
+ *   mul       [T, out] of io_dtype, rows ldmul apart, or NULL (factor 1).
+ *   residual  [T, out] of io_dtype, rows ldres apart, or NULL.
+ *   y         [T, out] of io_dtype, rows ldy apart.
+ * The product accumulates in fp32, the rest is fp32, and y is rounded once.
+ * x, mul, residual and y are 16-byte aligned and their row strides whole
+ * multiples of 16 bytes, at least a row long.  mul and residual may be y
+ * itself (same pointer and stride); y overlaps no other operand.  Columns of
+ * y's rows past `out` are left as they were. */
+typedef struct adafuse_linear_args {
+    int32_t layer;
+    int32_t target;
+    int32_t weight;      /* ADAFUSE_WEIGHT_* */
+    int32_t activation;  /* ADAFUSE_ACT_* */
+    int32_t io_dtype;    /* ADAFUSE_DTYPE_* of mul, residual and y */
+    int64_t T;
+    const void* x;
+    int64_t ldx;
+    const float* bias;
+    const void* mul;
+    int64_t ldmul;
+    const void* residual;
+    int64_t ldres;
+    void* y;
+    int64_t ldy;
+} adafuse_linear_args;
+
+/* y = residual + mul * act(x W^T + bias).  T == 0 is a no-op.  INVALID_ARG
+ * for a bad pointer, stride, layer, target or enum, or for
+ * ADAFUSE_WEIGHT_BASE without a registered base; UNSUPPORTED_SHAPE for T
+ * above 2^31 - 1.  One launch on `stream`. */
+ADAFUSE_API int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stream);
+
+/* Bytes of device workspace adafuse_linear_routed needs for T tokens on this
+ * weight (a multiple of 256; not decreasing in T).  Host-only. */
+ADAFUSE_API int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, int32_t target,
+                                         int64_t T, int32_t io_dtype, int64_t* bytes);
+
+/* y = residual + mul * act(x W^T + bias + s * sum_j gate_j (x A_e^T) B_e^T),
+ * e = idx_j, over the used slots of each token's own route record (`slots` 2,
+ * 4 or 8 as written by adafuse_pregate, adafuse_pregate_topk or
+ * adafuse_route_experts; 16-byte aligned).  The same expert in two slots
+ * counts with the sum of its gates.  A slot whose index is outside [-1, E) or
+ * whose gate is not finite raises ADAFUSE_STATUS_BAD_EXPERT / _BAD_GATE and
+ * counts as empty.  x A_e^T is accumulated in fp32; for ADAFUSE_DTYPE_BF16
+ * outputs its gated values may be carried as bf16, for ADAFUSE_DTYPE_F32 as
+ * two bf16 terms (relative 2^-17).  W is not changed.
+ * workspace: 256-byte aligned device memory of at least
+ * adafuse_linear_workspace bytes (INVALID_ARG otherwise); calls that may
+ * overlap on the GPU need workspaces of their own.  Its contents before and
+ * after the call mean nothing. */
+ADAFUSE_API int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args,
+                                      const void* routes, int32_t slots, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
+
 /* Tile edge of the segment table (128). */
 ADAFUSE_API int adafuse_tile_size(void);
 

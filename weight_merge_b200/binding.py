@@ -37,6 +37,18 @@ ADAFUSE_MAPS_PLAIN = 1
 ADAFUSE_MAPS_BLOCKED = 2
 ADAFUSE_MAX_TOP_K = 4
 ADAFUSE_MAX_BATCH_TOKENS = 4096
+ADAFUSE_DTYPE_BF16 = 0
+ADAFUSE_DTYPE_F32 = 1
+ADAFUSE_MAX_ROUTE_SLOTS = 8
+ADAFUSE_SCORE_SOFTMAX = 0
+ADAFUSE_SCORE_SIGMOID = 1
+ADAFUSE_WEIGHT_CURRENT = 0
+ADAFUSE_WEIGHT_BASE = 1
+ADAFUSE_ACT_NONE = 0
+ADAFUSE_ACT_RELU = 1
+ADAFUSE_ACT_GELU = 2
+ADAFUSE_ACT_GELU_TANH = 3
+ADAFUSE_ACT_SILU = 4
 
 
 class AdafuseError(RuntimeError):
@@ -54,6 +66,25 @@ class Route(ctypes.Structure):
 
 class Route4(ctypes.Structure):
     _fields_ = [("idx", ctypes.c_int32 * 4), ("gate", ctypes.c_float * 4)]
+
+
+class Route8(ctypes.Structure):
+    _fields_ = [("idx", ctypes.c_int32 * 8), ("gate", ctypes.c_float * 8)]
+
+
+class Gating(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int32), ("target", ctypes.c_int32), ("weight", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("T", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("ldmul", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldres", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
 class Target(ctypes.Structure):
@@ -111,6 +142,11 @@ def lib() -> ctypes.CDLL:
         "adafuse_debug_stall_next_switch": ([P], ctypes.c_int),
         "adafuse_debug_stall_next_switch_at": ([P, i32], ctypes.c_int),
         "adafuse_refresh_adapters": ([P, P], ctypes.c_int),
+        "adafuse_route_experts": ([P, P, i32, i64, i64, i64, P, ctypes.POINTER(Gating), i32, P, P],
+                                  ctypes.c_int),
+        "adafuse_linear": ([P, ctypes.POINTER(LinearArgs), P], ctypes.c_int),
+        "adafuse_linear_workspace": ([P, i32, i32, i64, i32, ctypes.POINTER(i64)], ctypes.c_int),
+        "adafuse_linear_routed": ([P, ctypes.POINTER(LinearArgs), P, i32, P, i64, P], ctypes.c_int),
         "adafuse_segment_table": ([ctypes.POINTER(Desc), P, i64, ctypes.POINTER(i64)], ctypes.c_int),
         "adafuse_tile_size": ([], ctypes.c_int),
         "adafuse_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -219,6 +255,31 @@ def adafuse_rebase_topk(ctx: int, cur: Optional[int], stream: int = 0) -> None:
     _check(lib().adafuse_rebase_topk(ctx, cur or None, stream or None), "adafuse_rebase_topk")
 
 
+def adafuse_route_experts(ctx: int, h: int, h_dtype: int, T: int, d: int, ldh: int, Wr: int,
+                          gating: Gating, slots: int, route: int, stream: int = 0) -> None:
+    _check(lib().adafuse_route_experts(ctx, h, int(h_dtype), int(T), int(d), int(ldh), Wr,
+                                       ctypes.byref(gating), int(slots), route, stream or None),
+           "adafuse_route_experts")
+
+
+def adafuse_linear(ctx: int, args: LinearArgs, stream: int = 0) -> None:
+    _check(lib().adafuse_linear(ctx, ctypes.byref(args), stream or None), "adafuse_linear")
+
+
+def adafuse_linear_workspace(ctx: int, layer: int, target: int, T: int, io_dtype: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().adafuse_linear_workspace(ctx, int(layer), int(target), int(T), int(io_dtype),
+                                          ctypes.byref(n)), "adafuse_linear_workspace")
+    return n.value
+
+
+def adafuse_linear_routed(ctx: int, args: LinearArgs, routes: int, slots: int, workspace: int,
+                          workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().adafuse_linear_routed(ctx, ctypes.byref(args), routes, int(slots), workspace,
+                                       int(workspace_bytes), stream or None),
+           "adafuse_linear_routed")
+
+
 def adafuse_refresh_adapters(ctx: int, stream: int = 0) -> None:
     _check(lib().adafuse_refresh_adapters(ctx, stream or None), "adafuse_refresh_adapters")
 
@@ -301,6 +362,36 @@ def make_desc(n_layers: int, n_targets: int, n_experts: int, rank: int, alpha: f
              ctypes.cast(arr, ctypes.POINTER(Target)))
     d._keep = (arr, names)
     return d
+
+
+def make_gating(score: int = ADAFUSE_SCORE_SOFTMAX, k: int = 2, n_groups: int = 1,
+                top_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                bias=None) -> Gating:
+    """bias: a device fp32 tensor of E values (kept alive by the returned struct) or None."""
+    if bias is not None:
+        _need(bias, "float32", "bias")
+    g = Gating(int(score), int(k), int(n_groups), int(top_groups), int(group_top), int(renorm),
+               float(scale), None if bias is None else bias.data_ptr())
+    g._keep = bias
+    return g
+
+
+def _need(t, dtype: str, what: str) -> None:
+    """A device tensor of the named torch dtype with unit stride along its last dimension."""
+    if str(t.dtype) != "torch." + dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not on a CUDA device")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+
+
+def _row_stride(t) -> int:
+    """Elements between row starts (a row's length when there is one row or none)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+_DTYPES = {"torch.bfloat16": ADAFUSE_DTYPE_BF16, "torch.float32": ADAFUSE_DTYPE_F32}
 
 
 class Switcher:
@@ -386,6 +477,80 @@ class Switcher:
 
     def rebase_topk(self, cur: Optional[int], stream: int = 0) -> None:
         adafuse_rebase_topk(self.ctx, cur, stream)
+
+    def route_experts(self, h, Wr, gating: Gating, routes, stream: int = 0) -> None:
+        """One decision per row of h [T, d] (bf16 or fp32) into ``routes``, an
+        int32 [T, 2 * slots] buffer of 2, 4 or 8 slots a record."""
+        T, d = h.shape
+        dtype = _DTYPES.get(str(h.dtype))
+        if dtype is None:
+            raise TypeError(f"h: dtype {h.dtype}, expected bfloat16 or float32")
+        _need(h, str(h.dtype)[6:], "h")
+        _need(Wr, "float32", "Wr")
+        _need(routes, "int32", "routes")
+        E = self.desc.n_experts
+        if tuple(Wr.shape) != (d, E) or not Wr.is_contiguous():
+            raise ValueError(f"Wr: shape {tuple(Wr.shape)}, expected a contiguous {(d, E)}")
+        if gating._keep is not None and gating._keep.numel() != E:
+            raise ValueError(f"bias: {gating._keep.numel()} values for {E} experts")
+        if routes.shape[0] != T or not routes.is_contiguous():
+            raise ValueError("routes: one contiguous record per row of h")
+        adafuse_route_experts(self.ctx, h.data_ptr(), dtype, T, d, _row_stride(h), Wr.data_ptr(),
+                              gating, routes.shape[1] // 2, routes.data_ptr(), stream)
+
+    def _linear_args(self, layer, target, x, y, bias, activation, mul, residual, base):
+        n_targets = self.desc.n_targets
+        if not (0 <= layer < self.n_layers and 0 <= target < n_targets):
+            raise ValueError(f"no weight ({layer}, {target})")
+        out, inn = self._tensors[0][layer * n_targets + target].shape
+        T = x.shape[0]
+        io = _DTYPES.get(str(y.dtype))
+        if io is None:
+            raise TypeError(f"y: dtype {y.dtype}, expected bfloat16 or float32")
+        _need(x, "bfloat16", "x")
+        if tuple(x.shape) != (T, inn):
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, inn)}")
+        for name, t in (("y", y), ("mul", mul), ("residual", residual)):
+            if t is not None:
+                _need(t, str(y.dtype)[6:], name)
+                if tuple(t.shape) != (T, out):
+                    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, out)}")
+        if bias is not None:
+            _need(bias, "float32", "bias")
+            if tuple(bias.shape) != (out,):
+                raise ValueError(f"bias: shape {tuple(bias.shape)}, expected {(out,)}")
+        p = lambda t: None if t is None else t.data_ptr()
+        ld = lambda t: 0 if t is None else _row_stride(t)
+        return LinearArgs(int(layer), int(target),
+                          ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT, int(activation),
+                          io, T, p(x), ld(x), p(bias), p(mul), ld(mul), p(residual), ld(residual),
+                          p(y), ld(y))
+
+    def linear(self, layer: int, target: int, x, y, bias=None, activation: int = ADAFUSE_ACT_NONE,
+               mul=None, residual=None, base: bool = False, stream: int = 0) -> None:
+        """y = residual + mul * act(x W^T + bias) with W of (layer, target), or
+        its registered pristine copy when ``base``."""
+        a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
+        adafuse_linear(self.ctx, a, stream)
+
+    def linear_workspace(self, layer: int, target: int, T: int, f32: bool = False) -> int:
+        """Workspace bytes of linear_routed for T tokens (``f32``: y is fp32)."""
+        return adafuse_linear_workspace(self.ctx, layer, target, T,
+                                        ADAFUSE_DTYPE_F32 if f32 else ADAFUSE_DTYPE_BF16)
+
+    def linear_routed(self, layer: int, target: int, x, routes, y, workspace, bias=None,
+                      activation: int = ADAFUSE_ACT_NONE, mul=None, residual=None,
+                      base: bool = False, stream: int = 0) -> None:
+        """linear() with each row's own gated experts from ``routes`` (int32
+        [T, 2 * slots]); workspace: a device uint8 tensor of at least
+        linear_workspace() bytes that no overlapping call uses."""
+        a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
+        _need(routes, "int32", "routes")
+        if routes.shape[0] != x.shape[0] or not routes.is_contiguous():
+            raise ValueError("routes: one contiguous record per row of x")
+        adafuse_linear_routed(self.ctx, a, routes.data_ptr(), routes.shape[1] // 2,
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              stream)
 
     def set_kernel(self, kernel: int) -> None:
         adafuse_set_switch_kernel(self.ctx, kernel)

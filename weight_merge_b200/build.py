@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libadafuse.so")
-SOURCES = ["adafuse_abi.cu", "noalloc.cu"]
+SOURCES = ["adafuse_abi.cu", "noalloc.cu", "forward.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -8,12 +8,12 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
-#include <mutex>
 #include <new>
 #include <vector>
 
 #include "adafuse.h"
 #include "common.cuh"
+#include "context.cuh"
 #include "pregate.cuh"
 #include "switch_mma.cuh"
 #include "switch_tc.cuh"
@@ -21,97 +21,23 @@
 
 using namespace adafuse;
 
-struct adafuse_ctx {
-    int device = 0;
-    int sm_count = 0;
-    int32_t n_layers = 0, n_targets = 0, n_experts = 0, rank = 0;
-    float alpha = 0.f, scale = 0.f;
-    int64_t n_tiles = 0;
-    std::vector<int64_t> layer_tile_begin;  // [n_layers + 1]
-    PairDesc* d_pairs = nullptr;
-    TileEntry* d_tiles = nullptr;
-    int32_t* d_status = nullptr;
-    CUtensorMap* d_maps = nullptr;  // kMapsPerPair per pair when the tensor-core kernel can run
-    bool blk = false;               // those maps are blocked (every weight's in % 64 == 0)
-    int tc_kp = 0;                  // its padded rank (16, 32, 64), 0 = not eligible
-    int kernel = ADAFUSE_KERNEL_AUTO;
-    std::vector<PairDesc> h_pairs;  // host copy of d_pairs (re-base pointers are patched in)
-    CUtensorMap* d_w0_maps = nullptr;  // 1 per pair on the re-base source W0
-    bool has_base = false;
-    int stall_at = 0;  // test hook: the next tensor-core launch stalls at each CTA's n-th tile
-    // pair kernel: 256 x 128 blocks, layer-major like the tile table
-    TileEntry* d_blocks = nullptr;
-    uint16_t* d_bpad = nullptr;              // rank < 8: B with rows zero-padded to 8
-    uint16_t* d_fold = nullptr;              // rank <= 8: folded-coefficient operands
-                                             // (allocated on first use, see ensure_fold)
-    bool fold_failed = false;                // that allocation failed: the kernel is off
-    float* d_logits = nullptr;               // [kMaxBatchTokens, E] batch pre-gate scratch
-    unsigned long long* d_sched = nullptr;   // [2] ticket counter of the dynamic tile schedule
-    int schedule = ADAFUSE_SCHEDULE_AUTO;
-    std::vector<int64_t> layer_block_begin;  // [n_layers + 1]
-    int pair_clusters = 0;                   // co-resident CTA pairs (0 = not queried yet)
-    int max_ctas = 0;                        // cap on a switch's persistent grid (0 = none)
-};
-
 namespace {
 
 thread_local char g_last_error[256] = "";
 
-int cuda_fail(cudaError_t e, const char* what) {
+}  // namespace
+
+int adafuse::cuda_fail(cudaError_t e, const char* what) {
     std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, cudaGetErrorString(e));
     return ADAFUSE_ERR_CUDA;
 }
 
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 // CTAs a switch launch may keep resident: every SM, or the caller's cap
 // (adafuse_set_max_ctas) so that other work can run beside the switch.
 int switch_ctas(const adafuse_ctx* c) {
     return c->max_ctas > 0 && c->max_ctas < c->sm_count ? c->max_ctas : c->sm_count;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Raise a kernel's dynamic shared-memory limit only when this device has not
-// been given at least `bytes` for that kernel yet (the host call is not free,
-// and the decode-time pre-gate launches are short).  Keyed by the kernel's
-// address and the device: kernels of one signature are different entries.
-struct SmemAttrEntry {
-    const void* fn;
-    int device;
-    size_t bytes;
-};
-
-template <typename Kernel>
-void ensure_smem_attr(Kernel kernel, size_t bytes, int device) {
-    static std::mutex mu;
-    static std::vector<SmemAttrEntry> done;
-    const void* fn = reinterpret_cast<const void*>(kernel);
-    std::lock_guard<std::mutex> lk(mu);
-    for (const SmemAttrEntry& en : done)
-        if (en.fn == fn && en.device == device && en.bytes >= bytes) return;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-        return;   // the launch reports the error
-    for (SmemAttrEntry& en : done)
-        if (en.fn == fn && en.device == device) {
-            en.bytes = bytes;
-            return;
-        }
-    done.push_back({fn, device, bytes});
 }
 
 // Shape and pointer checks shared by create and the host-only table query.

@@ -1,0 +1,176 @@
+// forward.cu -- C ABI of the per-token forward: routing to experts, the
+// product of a weight with a fused epilogue, and the product with every
+// token's own experts.  See include/adafuse.h for each contract.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "adafuse.h"
+#include "common.cuh"
+#include "context.cuh"
+#include "linear_common.cuh"
+#include "linear_simple.cuh"
+#include "route_experts.cuh"
+
+using namespace adafuse;
+
+namespace {
+
+bool slots_ok(int32_t slots) { return slots == 2 || slots == 4 || slots == 8; }
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// The weight (layer, target) of the context, or null.
+const PairDesc* find_pair(const adafuse_ctx* ctx, int32_t layer, int32_t target) {
+    if (layer < 0 || layer >= ctx->n_layers || target < 0 || target >= ctx->n_targets) return nullptr;
+    return &ctx->h_pairs[(size_t)((int64_t)layer * ctx->n_targets + target)];
+}
+
+// A [T, n] operand of `size`-byte elements with rows ld apart: 16-byte aligned
+// base, rows whole multiples of 16 bytes, at least n long.
+bool rows_ok(const void* p, int64_t ld, int64_t n, int64_t size) {
+    return p != nullptr && aligned16(p) && ld >= n && ld <= INT64_MAX / 16 && ld * size % 16 == 0;
+}
+
+// Checks of a product's arguments, and its launch parameters.
+int linear_params(const adafuse_ctx* ctx, const adafuse_linear_args* a, LinearParams* p) {
+    std::memset(p, 0, sizeof *p);
+    if (ctx == nullptr || a == nullptr) return ADAFUSE_ERR_INVALID_ARG;
+    const PairDesc* pd = find_pair(ctx, a->layer, a->target);
+    if (pd == nullptr || a->T < 0) return ADAFUSE_ERR_INVALID_ARG;
+    if (a->weight != ADAFUSE_WEIGHT_CURRENT && a->weight != ADAFUSE_WEIGHT_BASE)
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (a->weight == ADAFUSE_WEIGHT_BASE && !ctx->has_base) return ADAFUSE_ERR_INVALID_ARG;
+    if (a->activation < ADAFUSE_ACT_NONE || a->activation > ADAFUSE_ACT_SILU)
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (a->io_dtype != ADAFUSE_DTYPE_BF16 && a->io_dtype != ADAFUSE_DTYPE_F32)
+        return ADAFUSE_ERR_INVALID_ARG;
+    p->T = a->T;
+    if (a->T == 0) return ADAFUSE_OK;
+    if (a->T > INT32_MAX) return ADAFUSE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t size = a->io_dtype == ADAFUSE_DTYPE_F32 ? 4 : 2;
+    if (!rows_ok(a->x, a->ldx, pd->in, 2) || !rows_ok(a->y, a->ldy, pd->out, size))
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (a->mul != nullptr && !rows_ok(a->mul, a->ldmul, pd->out, size)) return ADAFUSE_ERR_INVALID_ARG;
+    if (a->residual != nullptr && !rows_ok(a->residual, a->ldres, pd->out, size))
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a->bias) & 3u) return ADAFUSE_ERR_INVALID_ARG;
+    p->x = static_cast<const uint16_t*>(a->x);
+    p->W = a->weight == ADAFUSE_WEIGHT_BASE ? pd->W0 : pd->W;
+    p->bias = a->bias;
+    p->mul = a->mul;
+    p->res = a->residual;
+    p->y = a->y;
+    p->ldx = a->ldx;
+    p->ldmul = a->ldmul;
+    p->ldres = a->ldres;
+    p->ldy = a->ldy;
+    p->out = pd->out;
+    p->in = pd->in;
+    p->act = a->activation;
+    p->f32 = a->io_dtype == ADAFUSE_DTYPE_F32;
+    p->status = ctx->d_status;
+    return ADAFUSE_OK;
+}
+
+int64_t workspace_bytes_for(const adafuse_ctx* ctx, int64_t T) {
+    return round_up(T * ctx->n_experts * ctx->rank * 4, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int64_t T, int64_t d,
+                          int64_t ldh, const float* Wr, const adafuse_gating* gating, int32_t slots,
+                          void* route, void* stream) {
+    if (ctx == nullptr || gating == nullptr) return ADAFUSE_ERR_INVALID_ARG;
+    if (h_dtype != ADAFUSE_DTYPE_BF16 && h_dtype != ADAFUSE_DTYPE_F32) return ADAFUSE_ERR_INVALID_ARG;
+    if (T < 0 || d < 4 || (d & 3) != 0 || (ldh & 3) != 0 || ldh < d || !slots_ok(slots))
+        return ADAFUSE_ERR_INVALID_ARG;
+    const adafuse_gating& q = *gating;
+    const int E = ctx->n_experts;
+    if (q.score != ADAFUSE_SCORE_SOFTMAX && q.score != ADAFUSE_SCORE_SIGMOID)
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (q.k < 1 || q.k > slots || q.n_groups < 1 || q.n_groups > E || E % q.n_groups != 0)
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (q.top_groups < 1 || q.top_groups > q.n_groups || q.group_top < 1 || q.group_top > 2)
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (!std::isfinite(q.scale) || (reinterpret_cast<uintptr_t>(q.bias) & 3u))
+        return ADAFUSE_ERR_INVALID_ARG;
+    if (T == 0) return ADAFUSE_OK;
+    if (h == nullptr || Wr == nullptr || route == nullptr || !aligned16(h) || !aligned16(route) ||
+        (reinterpret_cast<uintptr_t>(Wr) & 3u))
+        return ADAFUSE_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const GateParams g{q.score, q.k, q.n_groups, q.top_groups, q.group_top, q.renorm != 0,
+                       q.scale, q.bias, E, slots};
+    const unsigned grid = (unsigned)std::min<int64_t>(T, (int64_t)ctx->sm_count * 8);
+    int32_t* rt = static_cast<int32_t*>(route);
+    if (h_dtype == ADAFUSE_DTYPE_F32)
+        route_experts_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(h), T, d, ldh, Wr, g, rt);
+    else
+        route_experts_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(h), T, d, ldh, Wr,
+                                                  g, rt);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "route launch");
+}
+
+int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stream) {
+    LinearParams p;
+    const int rc = linear_params(ctx, args, &p);
+    if (rc != ADAFUSE_OK || p.T == 0) return rc;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    const dim3 grid((unsigned)ceil_div(p.out, kSimpleTile), (unsigned)ceil_div(p.T, kSimpleTile));
+    simple_linear_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "linear launch");
+}
+
+int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, int32_t target, int64_t T,
+                             int32_t io_dtype, int64_t* bytes) {
+    if (ctx == nullptr || bytes == nullptr || T < 0) return ADAFUSE_ERR_INVALID_ARG;
+    if (find_pair(ctx, layer, target) == nullptr) return ADAFUSE_ERR_INVALID_ARG;
+    if (io_dtype != ADAFUSE_DTYPE_BF16 && io_dtype != ADAFUSE_DTYPE_F32) return ADAFUSE_ERR_INVALID_ARG;
+    if (T > INT32_MAX) return ADAFUSE_ERR_UNSUPPORTED_SHAPE;
+    *bytes = workspace_bytes_for(ctx, T);
+    return ADAFUSE_OK;
+}
+
+int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, const void* routes,
+                          int32_t slots, void* workspace, int64_t workspace_bytes, void* stream) {
+    LinearParams p;
+    const int rc = linear_params(ctx, args, &p);
+    if (rc != ADAFUSE_OK) return rc;
+    if (!slots_ok(slots)) return ADAFUSE_ERR_INVALID_ARG;
+    if (p.T == 0) return ADAFUSE_OK;
+    if (routes == nullptr || !aligned16(routes)) return ADAFUSE_ERR_INVALID_ARG;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < workspace_bytes_for(ctx, p.T))
+        return ADAFUSE_ERR_INVALID_ARG;
+    const PairDesc* pd = find_pair(ctx, args->layer, args->target);
+    p.A = pd->A;
+    p.B = pd->B;
+    p.routes = static_cast<const int32_t*>(routes);
+    p.slots = slots;
+    p.E = ctx->n_experts;
+    p.r = ctx->rank;
+    p.s = ctx->scale;
+    p.z = static_cast<float*>(workspace);
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned gt = (unsigned)ceil_div(p.T, kSimpleTile);
+    simple_down_kernel<<<dim3((unsigned)ceil_div((int64_t)p.E * p.r, kSimpleTile), gt), 256, 0, s>>>(p);
+    simple_linear_kernel<<<dim3((unsigned)ceil_div(p.out, kSimpleTile), gt), 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "routed linear launch");
+}
+
+}  // extern "C"
