@@ -12,7 +12,7 @@
 #include "common.cuh"
 #include "context.cuh"
 #include "linear_common.cuh"
-#include "linear_simple.cuh"
+#include "linear_host.cuh"
 #include "route_experts.cuh"
 
 using namespace adafuse;
@@ -20,8 +20,6 @@ using namespace adafuse;
 namespace {
 
 bool slots_ok(int32_t slots) { return slots == 2 || slots == 4 || slots == 8; }
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // The weight (layer, target) of the context, or null.
 const PairDesc* find_pair(const adafuse_ctx* ctx, int32_t layer, int32_t target) {
@@ -76,10 +74,6 @@ int linear_params(const adafuse_ctx* ctx, const adafuse_linear_args* a, LinearPa
     return ADAFUSE_OK;
 }
 
-int64_t workspace_bytes_for(const adafuse_ctx* ctx, int64_t T) {
-    return round_up(T * ctx->n_experts * ctx->rank * 4, 256);
-}
-
 }  // namespace
 
 extern "C" {
@@ -127,19 +121,21 @@ int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stre
     if (rc != ADAFUSE_OK || p.T == 0) return rc;
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
-    const dim3 grid((unsigned)ceil_div(p.out, kSimpleTile), (unsigned)ceil_div(p.T, kSimpleTile));
-    simple_linear_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    TcLinear L;
+    std::memset(&L, 0, sizeof L);
+    L.p = p;
+    const cudaError_t e = launch_product(L, ctx, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "linear launch");
 }
 
 int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, int32_t target, int64_t T,
                              int32_t io_dtype, int64_t* bytes) {
     if (ctx == nullptr || bytes == nullptr || T < 0) return ADAFUSE_ERR_INVALID_ARG;
-    if (find_pair(ctx, layer, target) == nullptr) return ADAFUSE_ERR_INVALID_ARG;
+    const PairDesc* pd = find_pair(ctx, layer, target);
+    if (pd == nullptr) return ADAFUSE_ERR_INVALID_ARG;
     if (io_dtype != ADAFUSE_DTYPE_BF16 && io_dtype != ADAFUSE_DTYPE_F32) return ADAFUSE_ERR_INVALID_ARG;
     if (T > INT32_MAX) return ADAFUSE_ERR_UNSUPPORTED_SHAPE;
-    *bytes = workspace_bytes_for(ctx, T);
+    *bytes = routed_layout(ctx, *pd, T, io_dtype == ADAFUSE_DTYPE_F32).bytes;
     return ADAFUSE_OK;
 }
 
@@ -151,25 +147,42 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     if (!slots_ok(slots)) return ADAFUSE_ERR_INVALID_ARG;
     if (p.T == 0) return ADAFUSE_OK;
     if (routes == nullptr || !aligned16(routes)) return ADAFUSE_ERR_INVALID_ARG;
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        workspace_bytes < workspace_bytes_for(ctx, p.T))
-        return ADAFUSE_ERR_INVALID_ARG;
     const PairDesc* pd = find_pair(ctx, args->layer, args->target);
+    const RoutedLayout lay = routed_layout(ctx, *pd, p.T, p.f32 != 0);
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < lay.bytes)
+        return ADAFUSE_ERR_INVALID_ARG;
     p.A = pd->A;
-    p.B = pd->B;
+    p.B = pd->Bk;
     p.routes = static_cast<const int32_t*>(routes);
     p.slots = slots;
     p.E = ctx->n_experts;
     p.r = ctx->rank;
     p.s = ctx->scale;
-    p.z = static_cast<float*>(workspace);
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned gt = (unsigned)ceil_div(p.T, kSimpleTile);
-    simple_down_kernel<<<dim3((unsigned)ceil_div((int64_t)p.E * p.r, kSimpleTile), gt), 256, 0, s>>>(p);
-    simple_linear_kernel<<<dim3((unsigned)ceil_div(p.out, kSimpleTile), gt), 256, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    TcLinear L;
+    std::memset(&L, 0, sizeof L);
+    L.rp = lay.rp;
+    L.terms = lay.terms;
+    L.b_swizzled = lay.rp == 16 || lay.rp == 32 || lay.rp == 64;
+    L.b_one = lay.rp == 8;
+    L.v = static_cast<uint16_t*>(workspace);
+    if (lay.pad) {
+        uint16_t* padded = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + lay.v_bytes);
+        const int64_t nrows = (int64_t)p.E * p.out;
+        const unsigned grid =
+            (unsigned)std::min<int64_t>(ceil_div(nrows * lay.rp, 256), (int64_t)ctx->sm_count * 8);
+        pad_b_kernel<<<grid, 256, 0, s>>>(p.B, padded, nrows, p.r, lay.rp);
+        p.B = padded;
+    }
+    L.p = p;
+    L.bsteps = (int)ceil_div((int64_t)p.E * lay.rp, 64);
+    L.vsteps = L.terms * L.bsteps;
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_down(L, ctx, s);
+    if (e == cudaSuccess) e = launch_product(L, ctx, s);
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "routed linear launch");
 }
 

@@ -1,0 +1,167 @@
+// linear_host.cuh -- host side of the product kernels: tensor maps, the split
+// of the contraction, workspace layout and launches.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "context.cuh"
+#include "linear_skinny.cuh"
+
+namespace adafuse {
+
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+inline bool encode_map(CUtensorMap* m, int dims, const void* base, const cuuint64_t* dim,
+                       const cuuint64_t* stride_bytes, const cuuint32_t* box, CUtensorMapSwizzle sw) {
+    const EncodeTiledFn enc = encode_tiled_fn();
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc != nullptr &&
+           enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(base), dim,
+               stride_bytes, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [rows, cols] bf16, rows ld elements apart: boxes of 64 columns x box_rows,
+// 128-byte swizzle.
+inline bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                        int box_rows) {
+    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    return encode_map(m, 2, base, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// V [terms][T][width]: boxes of 64 columns x box_rows tokens of one term;
+// columns past the width read as zero.
+inline bool encode_v(CUtensorMap* m, const TcLinear& L, int box_rows) {
+    const int64_t width = (int64_t)L.p.E * L.rp;
+    const cuuint64_t dim[3] = {(cuuint64_t)width, (cuuint64_t)L.p.T, (cuuint64_t)L.terms};
+    const cuuint64_t stride[2] = {(cuuint64_t)width * 2, (cuuint64_t)(L.p.T * width * 2)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    return encode_map(m, 3, L.v, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The stacked B [E, out, rp] for load_b_step.
+inline bool encode_b(CUtensorMap* m, const TcLinear& L) {
+    const cuuint64_t rp = (cuuint64_t)L.rp, out = (cuuint64_t)L.p.out, E = (cuuint64_t)L.p.E;
+    if (L.b_swizzled) {
+        const cuuint64_t dim[3] = {rp, out, E};
+        const cuuint64_t stride[2] = {rp * 2, out * rp * 2};
+        const cuuint32_t box[3] = {(cuuint32_t)rp, 128, (cuuint32_t)(64 / rp)};
+        return encode_map(m, 3, L.p.B, dim, stride, box,
+                          rp == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                   : rp == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    const cuuint64_t dim[4] = {8, out, rp / 8, E};
+    const cuuint64_t stride[3] = {rp * 2, 16, out * rp * 2};
+    const cuuint32_t box[4] = {8, 128, 1, L.b_one ? 8u : 1u};
+    return encode_map(m, 4, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Workspace of a routed product: V, then (ranks above 8 that are not
+// multiples of 8) the padded copy of B.
+struct RoutedLayout {
+    int rp, terms;
+    bool pad;          // B is padded per call
+    int64_t v_bytes, bytes;
+};
+
+inline RoutedLayout routed_layout(const adafuse_ctx* ctx, const PairDesc& pd, int64_t T, bool f32) {
+    RoutedLayout w;
+    w.rp = (int)round_up(ctx->rank, 8);
+    w.terms = f32 ? 2 : 1;
+    w.pad = ctx->rank % 8 != 0 && pd.Bk == pd.B;
+    w.v_bytes = round_up((int64_t)w.terms * T * ctx->n_experts * w.rp * 2, 256);
+    w.bytes = w.v_bytes;
+    if (w.pad && T > 0) w.bytes += round_up((int64_t)ctx->n_experts * pd.out * w.rp * 2, 256);
+    return w;
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t smem, int cluster, bool overlap,
+                            cudaStream_t s, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = (unsigned)n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Cluster size of the skinny kernel: the contraction is split while the grid
+// stays within two CTAs an SM and every CTA keeps at least four steps.
+inline int skinny_split(int64_t tiles, int nsteps, int sm_count) {
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= 2 * (int64_t)sm_count && nsteps / (S * 2) >= 4) S *= 2;
+    return S;
+}
+
+template <int TN, int MODE>
+cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMap& map_b, bool overlap,
+                          const adafuse_ctx* ctx, cudaStream_t s) {
+    using C = SkinnyConfig<TN>;
+    CUtensorMap map_x, map_v;
+    std::memset(&map_v, 0, sizeof map_v);
+    if (!encode_rows(&map_x, L.p.x, L.p.T, L.p.in, L.p.ldx, TN)) return cudaErrorInvalidValue;
+    if (L.vsteps > 0 && !encode_v(&map_v, L, TN)) return cudaErrorInvalidValue;
+    L.tok_tiles = (int)ceil_div(L.p.T, TN);
+    const int64_t tiles = ceil_div(L.rows, 128) * L.tok_tiles;
+    const int S = skinny_split(tiles, L.xsteps + L.vsteps, ctx->sm_count);
+    if (tiles * S > INT32_MAX) return cudaErrorInvalidConfiguration;
+    auto kernel = linear_skinny_kernel<TN, MODE>;
+    ensure_smem_attr(kernel, C::kSmemBytes, ctx->device);
+    return launch_clusters(kernel, tiles * S, kSkinnyThreads, C::kSmemBytes, S, overlap, s, L, map_w, map_x,
+                           map_b, map_v, S);
+}
+
+template <int MODE>
+cudaError_t launch_skinny_any(const TcLinear& L, const CUtensorMap& map_w, const CUtensorMap& map_b,
+                              bool overlap, const adafuse_ctx* ctx, cudaStream_t s) {
+    const int64_t T = L.p.T;
+    if (T <= 16) return launch_skinny<16, MODE>(L, map_w, map_b, overlap, ctx, s);
+    if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, overlap, ctx, s);
+    if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, overlap, ctx, s);
+    return launch_skinny<128, MODE>(L, map_w, map_b, overlap, ctx, s);
+}
+
+// y of one product; L carries V's geometry when the adapters are part of it.
+inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
+    CUtensorMap map_w, map_b;
+    std::memset(&map_b, 0, sizeof map_b);
+    if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
+    if (L.vsteps > 0 && !encode_b(&map_b, L)) return cudaErrorInvalidValue;
+    L.rows = L.p.out;
+    L.xsteps = (int)ceil_div(L.p.in, 64);
+    return launch_skinny_any<kProduct>(L, map_w, map_b, L.vsteps > 0, ctx, s);
+}
+
+// V of a routed product.
+inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
+    CUtensorMap map_a, none;
+    std::memset(&none, 0, sizeof none);
+    L.rows = L.p.E * L.p.r;
+    L.xsteps = (int)ceil_div(L.p.in, 64);
+    L.vsteps = 0;
+    if (!encode_rows(&map_a, L.p.A, L.rows, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
+    return launch_skinny_any<kDown>(L, map_a, none, false, ctx, s);
+}
+
+}  // namespace adafuse

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "context.cuh"
 #include "switch_fold.cuh"
 #include "switch_tc.cuh"
 #include "switch_tc2.cuh"
@@ -20,26 +21,6 @@ inline int tc_kp_for(int r) {
     if (r < 1 || r > 64) return 0;
     if (r < 8) return 16;
     return r % 8 != 0 ? 0 : r <= 16 ? 16 : r <= 32 ? 32 : 64;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-inline EncodeTiledFn encode_tiled_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    }
-    return fn;
 }
 
 // Blocked maps (one TMA operation per W tile and per expert's A columns)
