@@ -121,10 +121,13 @@ int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stre
     if (rc != ADAFUSE_OK || p.T == 0) return rc;
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     TcLinear L;
     std::memset(&L, 0, sizeof L);
     L.p = p;
-    const cudaError_t e = launch_product(L, ctx, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = p.T <= kStreamMaxTokens
+                              ? launch_stream<kProduct>(p, p.W, p.out, nullptr, ctx, s)
+                              : launch_product(L, ctx, s);
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "linear launch");
 }
 
@@ -153,7 +156,7 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
         workspace_bytes < lay.bytes)
         return ADAFUSE_ERR_INVALID_ARG;
     p.A = pd->A;
-    p.B = pd->Bk;
+    p.B = pd->B;
     p.routes = static_cast<const int32_t*>(routes);
     p.slots = slots;
     p.E = ctx->n_experts;
@@ -162,6 +165,13 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.T <= kStreamMaxTokens) {
+        float* u = static_cast<float*>(workspace);
+        cudaError_t e = launch_stream<kDown>(p, p.A, p.E * p.r, u, ctx, s);
+        if (e == cudaSuccess) e = launch_stream<kRouted>(p, p.W, p.out, u, ctx, s);
+        return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "routed linear launch");
+    }
+    p.B = pd->Bk;   // rows of a multiple of 8 columns
     TcLinear L;
     std::memset(&L, 0, sizeof L);
     L.rp = lay.rp;

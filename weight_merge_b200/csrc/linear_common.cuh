@@ -26,7 +26,6 @@ struct LinearParams {
     const int32_t* routes;
     int slots, E, r;
     float s;
-    float* z;             // workspace [T, E * r] fp32: x A^T
     int32_t* status;
 };
 

@@ -10,6 +10,7 @@
 
 #include "context.cuh"
 #include "linear_skinny.cuh"
+#include "linear_stream.cuh"
 
 namespace adafuse {
 
@@ -62,7 +63,8 @@ inline bool encode_b(CUtensorMap* m, const TcLinear& L) {
     return encode_map(m, 4, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Workspace of a routed product: V, then (ranks above 8 that are not
+// Workspace of a routed product: V (or, for few tokens, u = x A^T in fp32: four
+// bytes a value cover either), then (ranks above 8 that are not
 // multiples of 8) the padded copy of B.
 struct RoutedLayout {
     int rp, terms;
@@ -75,7 +77,7 @@ inline RoutedLayout routed_layout(const adafuse_ctx* ctx, const PairDesc& pd, in
     w.rp = (int)round_up(ctx->rank, 8);
     w.terms = f32 ? 2 : 1;
     w.pad = ctx->rank % 8 != 0 && pd.Bk == pd.B;
-    w.v_bytes = round_up((int64_t)w.terms * T * ctx->n_experts * w.rp * 2, 256);
+    w.v_bytes = round_up(T * ctx->n_experts * w.rp * 4, 256);
     w.bytes = w.v_bytes;
     if (w.pad && T > 0) w.bytes += round_up((int64_t)ctx->n_experts * pd.out * w.rp * 2, 256);
     return w;
@@ -140,6 +142,33 @@ cudaError_t launch_skinny_any(const TcLinear& L, const CUtensorMap& map_w, const
     if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, overlap, ctx, s);
     if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, overlap, ctx, s);
     return launch_skinny<128, MODE>(L, map_w, map_b, overlap, ctx, s);
+}
+
+// Grid of the stream kernel: two CTAs an SM less `reserve` CTAs, or, where
+// there are few units, clusters of S <= 8 CTAs that share a unit's columns
+// while every warp keeps a step.
+inline int stream_grid(int rows, int in, int reserve, int sm_count, int* S) {
+    const int units = (int)ceil_div(rows, kStreamRows);
+    *S = 1;
+    while (*S < 8 && units * *S * 2 <= 2 * sm_count && in >= 64 * kStreamWarps * 2 * *S) *S *= 2;
+    if (*S > 1) return units * *S;
+    return std::max(1, std::min((int)ceil_div(rows, 4), 2 * sm_count - reserve));
+}
+
+// At most kStreamMaxTokens tokens.  kRouted overlaps the kDown launch before
+// it and leaves that launch's CTAs their places.
+template <int MODE>
+cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, float* u, const adafuse_ctx* ctx,
+                          cudaStream_t s) {
+    int S = 1, reserve = 0;
+    if (MODE == kRouted) reserve = std::min(stream_grid(p.E * p.r, p.in, 0, ctx->sm_count, &S), ctx->sm_count);
+    const int grid = stream_grid(rows, p.in, reserve, ctx->sm_count, &S);
+    const bool overlap = MODE == kRouted;
+    const bool wide = p.in % 16 == 0 && (reinterpret_cast<uintptr_t>(W) & 31u) == 0;
+    return wide ? launch_clusters(linear_stream_kernel<MODE, true>, grid, kStreamThreads, 0, S, overlap, s, p,
+                                  W, rows, u, S)
+                : launch_clusters(linear_stream_kernel<MODE, false>, grid, kStreamThreads, 0, S, overlap, s, p,
+                                  W, rows, u, S);
 }
 
 // y of one product; L carries V's geometry when the adapters are part of it.

@@ -25,6 +25,7 @@
 #include <cuda.h>
 
 #include "linear_common.cuh"
+#include "linear_stream.cuh"
 #include "sm100_ptx.cuh"
 
 namespace adafuse {
@@ -47,13 +48,6 @@ struct TcLinear {
 
 constexpr int kSkinnyThreads = 192;
 constexpr uint64_t kLinearWaitNs = 1000000000ull;   // 1 s per wait
-
-enum : int { kProduct = 0, kDown = 1 };
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
