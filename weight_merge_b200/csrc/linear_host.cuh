@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "context.cuh"
+#include "linear_pair.cuh"
 #include "linear_skinny.cuh"
 #include "linear_stream.cuh"
 
@@ -46,20 +47,20 @@ inline bool encode_v(CUtensorMap* m, const TcLinear& L, int box_rows) {
     return encode_map(m, 3, L.v, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The stacked B [E, out, rp] for load_b_step.
-inline bool encode_b(CUtensorMap* m, const TcLinear& L) {
+// The stacked B [E, out, rp] for load_b_step on nrow rows.
+inline bool encode_b(CUtensorMap* m, const TcLinear& L, int nrow) {
     const cuuint64_t rp = (cuuint64_t)L.rp, out = (cuuint64_t)L.p.out, E = (cuuint64_t)L.p.E;
     if (L.b_swizzled) {
         const cuuint64_t dim[3] = {rp, out, E};
         const cuuint64_t stride[2] = {rp * 2, out * rp * 2};
-        const cuuint32_t box[3] = {(cuuint32_t)rp, 128, (cuuint32_t)(64 / rp)};
+        const cuuint32_t box[3] = {(cuuint32_t)rp, (cuuint32_t)nrow, (cuuint32_t)(64 / rp)};
         return encode_map(m, 3, L.p.B, dim, stride, box,
                           rp == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
                                    : rp == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     }
     const cuuint64_t dim[4] = {8, out, rp / 8, E};
     const cuuint64_t stride[3] = {rp * 2, 16, out * rp * 2};
-    const cuuint32_t box[4] = {8, 128, 1, L.b_one ? 8u : 1u};
+    const cuuint32_t box[4] = {8, (cuuint32_t)nrow, 1, L.b_one ? 8u : 1u};
     return encode_map(m, 4, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
@@ -171,15 +172,38 @@ cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, fl
                                   W, rows, u, S);
 }
 
+template <int BN, bool CHUNKED>
+cudaError_t launch_pair(TcLinear L, bool overlap, const adafuse_ctx* ctx, cudaStream_t s) {
+    using C = PairConfig<BN>;
+    CUtensorMap map_w, map_x, map_b, map_v;
+    std::memset(&map_b, 0, sizeof map_b);
+    std::memset(&map_v, 0, sizeof map_v);
+    if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, BN / 2) ||
+        !encode_rows(&map_x, L.p.x, L.p.T, L.p.in, L.p.ldx, 128))
+        return cudaErrorInvalidValue;
+    if (L.vsteps > 0 && (!encode_b(&map_b, L, BN / 2) || !encode_v(&map_v, L, 128)))
+        return cudaErrorInvalidValue;
+    L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
+    const int64_t tiles = L.tok_tiles * ceil_div(L.p.out, BN);
+    auto kernel = linear_pair_kernel<BN, CHUNKED>;
+    ensure_smem_attr(kernel, C::kSmemBytes, ctx->device);
+    const int64_t pairs = std::min<int64_t>(tiles, ctx->sm_count / 2);
+    return launch_clusters(kernel, 2 * pairs, kPairThreads, C::kSmemBytes, 2, overlap, s, L, map_w, map_x,
+                           map_b, map_v);
+}
+
 // y of one product; L carries V's geometry when the adapters are part of it.
 inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
+    L.rows = L.p.out;
+    L.xsteps = (int)ceil_div(L.p.in, 64);
+    const bool overlap = L.vsteps > 0;
+    if (L.p.T > 128)
+        return L.p.f32 ? launch_pair<256, true>(L, overlap, ctx, s) : launch_pair<256, false>(L, overlap, ctx, s);
     CUtensorMap map_w, map_b;
     std::memset(&map_b, 0, sizeof map_b);
     if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
-    if (L.vsteps > 0 && !encode_b(&map_b, L)) return cudaErrorInvalidValue;
-    L.rows = L.p.out;
-    L.xsteps = (int)ceil_div(L.p.in, 64);
-    return launch_skinny_any<kProduct>(L, map_w, map_b, L.vsteps > 0, ctx, s);
+    if (L.vsteps > 0 && !encode_b(&map_b, L, 128)) return cudaErrorInvalidValue;
+    return launch_skinny_any<kProduct>(L, map_w, map_b, overlap, ctx, s);
 }
 
 // V of a routed product.

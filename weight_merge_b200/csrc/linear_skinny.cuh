@@ -38,8 +38,8 @@ struct TcLinear {
     int bsteps;        // 64-column steps of E * rp (vsteps = terms * bsteps)
     int rp;            // rank padded to a multiple of 8
     int terms;         // bf16 terms of V
-    int b_swizzled;    // rp is 16, 32 or 64: B arrives as [64 / rp][128][rp] swizzled tiles;
-                       // otherwise as eight [128][8] groups
+    int b_swizzled;    // rp is 16, 32 or 64: B arrives as [64 / rp][rows][rp] swizzled tiles;
+                       // otherwise as eight [rows][8] groups
     int b_one;         // the eight groups of a step come by one load (rp == 8)
     uint16_t* v;       // [terms][T][E * rp]
     int rows;          // kDown: E * r; otherwise out
@@ -47,7 +47,22 @@ struct TcLinear {
 };
 
 constexpr int kSkinnyThreads = 192;
-constexpr uint64_t kLinearWaitNs = 1000000000ull;   // 1 s per wait
+
+// Wait for the phase with the given parity; gives up after `limit` clocks or
+// once *abort is set.  Bounded by the SM's own clock, read every few polls:
+// the global timer costs enough per read to pace these short waits.
+constexpr long long kWaitClocks = 2000000000ll;   // about 1 s
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           long long limit = kWaitClocks) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (sm100::mbar_try_wait(bar, parity)) return true;
+        if (*abort || clock64() - t0 > limit) return false;
+    }
+}
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
@@ -57,10 +72,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// Loads of one 64-column step of the stacked B for 128 out rows from `row0`:
-// columns 64 * c .. of the E * rp stacked ones.  Experts past E read as zero.
+// Loads of one 64-column step of the stacked B for `nrow` (128 or 64) out rows
+// from row0: columns 64 * c .. of the E * rp stacked ones.  Experts past E read
+// as zero.
 template <typename Load3, typename Load4>
-__device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, uint8_t* dst,
+__device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, int nrow, uint8_t* dst,
                                             Load3&& load3, Load4&& load4) {
     if (L.b_swizzled) {
         load3(dst, 0, row0, c * (64 / L.rp));
@@ -71,70 +87,18 @@ __device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, 
 #pragma unroll 1
         for (int j = 0; j < 8; ++j) {
             const int grp = c * 8 + j;
-            load4(dst + j * 2048, 0, row0, grp % per, grp / per);
+            load4(dst + j * 16 * nrow, 0, row0, grp % per, grp / per);
         }
     }
 }
 
 // Descriptor of the 16-column piece k of such a step.
-__device__ __forceinline__ uint64_t b_step_desc(const TcLinear& L, uint32_t base, int k) {
+__device__ __forceinline__ uint64_t b_step_desc(const TcLinear& L, uint32_t base, uint32_t nrow, int k) {
     using namespace sm100;
-    if (!L.b_swizzled) return smem_desc(base + 4096u * k, 2048, 128, kSwizzleNone);
+    if (!L.b_swizzled) return smem_desc(base + 32u * nrow * k, 16u * nrow, 128, kSwizzleNone);
     const uint32_t sub = (16u * k) / (uint32_t)L.rp, in = (16u * k) % (uint32_t)L.rp;
-    return smem_desc(base + sub * 256u * L.rp + in * 2u, 16, 16u * L.rp,
+    return smem_desc(base + sub * 2u * nrow * L.rp + in * 2u, 16, 16u * L.rp,
                      L.rp == 16 ? kSwizzle32B : L.rp == 32 ? kSwizzle64B : kSwizzle128B);
-}
-
-// Eight consecutive columns of y for token t, from o (a multiple of 8): loads
-// of the factor and the residual as 16-byte vectors, one rounding, one store.
-__device__ __forceinline__ void finish8(const LinearParams& p, int64_t t, int o, float (&v)[8]) {
-    if (p.bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += __ldg(p.bias + o + i);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = apply_act(v[i], p.act);
-    auto load8 = [&](const void* base, int64_t ld, float (&w)[8]) {
-        if (p.f32) {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(base) + t * ld + o);
-            const float4 a = q[0], b = q[1];
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + t * ld + o);
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[2 * i] = __uint_as_float(u[i] << 16);
-                w[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
-        }
-    };
-    float w[8];
-    if (p.mul != nullptr) {
-        load8(p.mul, p.ldmul, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= w[i];
-    }
-    if (p.res != nullptr) {
-        load8(p.res, p.ldres, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += w[i];
-    }
-    if (p.f32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.y) + t * p.ldy + o);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + t * p.ldy + o) =
-            make_uint4(u[0], u[1], u[2], u[3]);
-    }
 }
 
 // The gate of expert e for token t times s: the sum over the record's slots
@@ -253,7 +217,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             uint32_t ph = 0;
 #pragma unroll 1
             for (int i = k0; i < k1; ++i) {
-                if (!mbar_wait_bounded(&empty[st], ph ^ 1, abort_flag, kLinearWaitNs)) { fail(); break; }
+                if (!wait_phase(&empty[st], ph ^ 1, abort_flag)) { fail(); break; }
                 uint8_t* w_dst = ring + (size_t)st * C::kStageBytes;
                 uint8_t* x_dst = w_dst + C::kWBytes;
                 uint64_t* bar = &full[st];
@@ -263,7 +227,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
                     tma_load_2d(x_dst, &map_x, i * 64, (int)tok0, bar);
                 } else {
                     const int vi = i - L.xsteps;
-                    load_b_step(L, vi % L.bsteps, row0, w_dst,
+                    load_b_step(L, vi % L.bsteps, row0, 128, w_dst,
                                 [&](void* d, int a, int b, int c) { tma_load_3d(d, &map_b, a, b, c, bar); },
                                 [&](void* d, int a, int b, int c, int e) {
                                     tma_load_4d(d, &map_b, a, b, c, e, bar);
@@ -286,7 +250,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             bool ok = true;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                if (!mbar_wait_bounded(&full[st], ph, abort_flag, kLinearWaitNs)) { fail(); ok = false; break; }
+                if (!wait_phase(&full[st], ph, abort_flag)) { fail(); ok = false; break; }
                 const int a = (int)((int64_t)i * naccs / n);   // accumulator a sums a run of steps
                 const bool first = a != acc;
                 acc = a;
@@ -295,7 +259,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
                 const bool adapters = k0 + i >= L.xsteps;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint64_t da = adapters ? b_step_desc(L, w_s, k)
+                    const uint64_t da = adapters ? b_step_desc(L, w_s, 128, k)
                                                  : smem_desc(w_s + 32u * k, 16, 1024, kSwizzle128B);
                     const uint64_t db = smem_desc(x_s + 32u * k, 16, 1024, kSwizzle128B);
                     tc_mma_f16(tmem + (uint32_t)(a * TN), da, db, idesc, !(first && k == 0));
@@ -311,7 +275,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     // ---- the CTA's partial tile into shared memory: part[token][128 rows]
     float* part = reinterpret_cast<float*>(ring);
     if (warp < 4) {
-        const bool ok = mbar_wait_bounded(acc_full, 0, abort_flag, 4 * kLinearWaitNs);
+        const bool ok = wait_phase(acc_full, 0, abort_flag, 4 * kWaitClocks);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
@@ -386,7 +350,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             if constexpr (MODE == kDown)
                 finish_down8(L, tok0 + tok, row0 + r8, v, bad);
             else
-                finish8(L.p, tok0 + tok, row0 + r8, v);
+                finish_cols<8>(L.p, tok0 + tok, row0 + r8, v);
         }
         if (MODE == kDown && bad != 0) atomicOr(L.p.status, bad);
     } else {
