@@ -177,7 +177,6 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     L.rp = lay.rp;
     L.terms = lay.terms;
     L.b_swizzled = lay.rp == 16 || lay.rp == 32 || lay.rp == 64;
-    L.b_one = lay.rp == 8;
     L.v = static_cast<uint16_t*>(workspace);
     if (lay.pad) {
         uint16_t* padded = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + lay.v_bytes);

@@ -58,9 +58,17 @@ inline bool encode_b(CUtensorMap* m, const TcLinear& L, int nrow) {
                           rp == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
                                    : rp == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     }
+    if (rp == 8) {
+        // [E, out, 8] seen as [E][out / 8][64]: lines of 128 bytes that land as
+        // the same [8 experts][nrow][8]
+        const cuuint64_t dim[3] = {64, out / 8, E};
+        const cuuint64_t stride[2] = {128, out * 16};
+        const cuuint32_t box[3] = {64, (cuuint32_t)(nrow / 8), 8};
+        return encode_map(m, 3, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
     const cuuint64_t dim[4] = {8, out, rp / 8, E};
     const cuuint64_t stride[3] = {rp * 2, 16, out * rp * 2};
-    const cuuint32_t box[4] = {8, (cuuint32_t)nrow, 1, L.b_one ? 8u : 1u};
+    const cuuint32_t box[4] = {8, (cuuint32_t)nrow, 1, 1};
     return encode_map(m, 4, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 

@@ -19,7 +19,7 @@
 // Routed products: after x and W come V and the stacked B, as in
 // linear_skinny.cuh.
 //
-// Warps: 0 loads, 1 MMA (even CTA) and TMEM, 4..11 epilogue (token = 32 *
+// Warps: 0 and 2 loads, 1 MMA (even CTA) and TMEM, 4..11 epilogue (token = 32 *
 // (warp % 4) + lane, half of the columns each four warps).
 #pragma once
 
@@ -64,11 +64,11 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t q = cluster_ctarank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&full[i], 2);     // one arrival, with its bytes, from each CTA
+            mbar_init(&full[i], 4);     // one arrival, with its bytes, from each loading warp
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -100,8 +100,12 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     const int64_t tiles = (int64_t)L.tok_tiles * col_tiles;
     const int64_t t_first = cluster_id_x(), t_stride = cluster_count_x();
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
+        // two warps, since one thread's TMA operations start about 120 clocks
+        // apart: x and V (warp 0), W and B (warp 2)
         if (lane == 0) {
+            const bool left = warp == 0;
+            const uint32_t bytes = left ? C::kXBytes : C::kWBytes;
             const uint32_t full0 = cluster_addr(full, 0);
             bool waited = false, ok = true;
             int st = 0;
@@ -112,25 +116,27 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
 #pragma unroll 1
                 for (int i = 0; i < nsteps; ++i) {
                     if (!wait_phase(&empty[st], ph ^ 1, abort_flag)) { ok = false; break; }
-                    uint8_t* x_dst = ring + (size_t)st * C::kStageBytes;
-                    uint8_t* w_dst = x_dst + C::kXBytes;
+                    uint8_t* dst = ring + (size_t)st * C::kStageBytes + (left ? 0u : C::kXBytes);
                     const uint32_t bar = full0 + 8u * (uint32_t)st;
-                    mbar_arrive_expect_tx_cluster(bar, C::kStageBytes);
-                    if (i < L.xsteps) {
-                        tma_load_2d_pair(x_dst, &map_x, i * 64, tok0, bar);
-                        tma_load_2d_pair(w_dst, &map_w, i * 64, row0, bar);
+                    const int vi = i - L.xsteps;
+                    if (left && vi >= 0 && !waited) {
+                        pdl_wait();   // V is written by the launch before
+                        waited = true;
+                    }
+                    mbar_arrive_expect_tx_cluster(bar, bytes);
+                    if (vi < 0) {
+                        if (left)
+                            tma_load_2d_pair(dst, &map_x, i * 64, tok0, bar);
+                        else
+                            tma_load_2d_pair(dst, &map_w, i * 64, row0, bar);
+                    } else if (left) {
+                        tma_load_3d_pair(dst, &map_v, (vi % L.bsteps) * 64, tok0, vi / L.bsteps, bar);
                     } else {
-                        const int vi = i - L.xsteps;
-                        load_b_step(L, vi % L.bsteps, row0, BN / 2, w_dst,
+                        load_b_step(L, vi % L.bsteps, row0, BN / 2, dst,
                                     [&](void* d, int a, int b, int c) { tma_load_3d_pair(d, &map_b, a, b, c, bar); },
                                     [&](void* d, int a, int b, int c, int e) {
                                         tma_load_4d_pair(d, &map_b, a, b, c, e, bar);
                                     });
-                        if (!waited) {
-                            pdl_wait();   // V is written by the launch before
-                            waited = true;
-                        }
-                        tma_load_3d_pair(x_dst, &map_v, (vi % L.bsteps) * 64, tok0, vi / L.bsteps, bar);
                     }
                     if (++st == C::kStages) { st = 0; ph ^= 1; }
                 }
@@ -145,8 +151,12 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && q == 0) {
+        // the whole warp walks the steps, so that descriptors are warp-uniform,
+        // and one elected lane issues
+        if (q == 0) {
             constexpr uint32_t idesc = instr_desc_bf16(kPairTokens, BN, 0);
+            const StepDesc rows = row_step_desc(), stacked = b_step_desc(L, BN / 2);
+            const uint32_t ring_s = smem_u32(ring);
             int st = 0, buf = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
@@ -156,24 +166,31 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
                     const bool begins = CHUNKED ? i % kChunkSteps == 0 : i == 0;
                     const bool ends = i == nsteps - 1 || (CHUNKED && i % kChunkSteps == kChunkSteps - 1);
                     if (begins) {
-                        if (!wait_phase(&acc_empty[buf], aph ^ 1, abort_flag)) { ok = false; break; }
+                        ok = __all_sync(0xffffffffu, wait_phase(&acc_empty[buf], aph ^ 1, abort_flag));
+                        if (!ok) break;
                         tc_fence_after();
                     }
-                    if (!wait_phase(&full[st], ph, abort_flag)) { ok = false; break; }
-                    const uint32_t x_s = smem_u32(ring + (size_t)st * C::kStageBytes);
-                    const uint32_t w_s = x_s + C::kXBytes;
-                    const bool adapters = i >= L.xsteps;
+                    ok = __all_sync(0xffffffffu, wait_phase(&full[st], ph, abort_flag));
+                    if (!ok) break;
+                    const uint32_t x_s = ring_s + (uint32_t)st * C::kStageBytes, w_s = x_s + C::kXBytes;
+                    const uint32_t d = tmem + (uint32_t)(buf * BN);
+                    if (elect_one()) {
+                        if (i < L.xsteps) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t da = smem_desc(x_s + 32u * k, 16, 1024, kSwizzle128B);
-                        const uint64_t db = adapters ? b_step_desc(L, w_s, BN / 2, k)
-                                                     : smem_desc(w_s + 32u * k, 16, 1024, kSwizzle128B);
-                        tc_mma_f16_pair(tmem + (uint32_t)(buf * BN), da, db, idesc, !(begins && k == 0));
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_f16_pair(d, rows.at(x_s, k), rows.at(w_s, k), idesc, !(begins && k == 0));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_f16_pair(d, rows.at(x_s, k), stacked.at(w_s, k), idesc,
+                                                !(begins && k == 0));
+                        }
+                        tc_commit_pair(&empty[st], 0x3);
+                        if (ends) tc_commit_pair(&acc_full[buf], 0x3);
                     }
-                    tc_commit_pair(&empty[st], 0x3);
+                    __syncwarp();
                     if (++st == C::kStages) { st = 0; ph ^= 1; }
                     if (ends) {
-                        tc_commit_pair(&acc_full[buf], 0x3);
                         buf ^= 1;
                         if (buf == 0) aph ^= 1;
                     }
@@ -181,7 +198,6 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
             }
             if (!ok) fail();
         }
-        __syncwarp();
     } else if (warp >= 4) {
         const int half = (warp - 4) >> 2;                 // which BN/2 columns
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * (BN / 2));

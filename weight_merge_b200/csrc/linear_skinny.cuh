@@ -40,13 +40,12 @@ struct TcLinear {
     int terms;         // bf16 terms of V
     int b_swizzled;    // rp is 16, 32 or 64: B arrives as [64 / rp][rows][rp] swizzled tiles;
                        // otherwise as eight [rows][8] groups
-    int b_one;         // the eight groups of a step come by one load (rp == 8)
     uint16_t* v;       // [terms][T][E * rp]
     int rows;          // kDown: E * r; otherwise out
     int tok_tiles;     // token tiles
 };
 
-constexpr int kSkinnyThreads = 192;
+constexpr int kSkinnyThreads = 224;
 
 // Wait for the phase with the given parity; gives up after `limit` clocks or
 // once *abort is set.  Bounded by the SM's own clock, read every few polls:
@@ -80,8 +79,9 @@ __device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, 
                                             Load3&& load3, Load4&& load4) {
     if (L.b_swizzled) {
         load3(dst, 0, row0, c * (64 / L.rp));
-    } else if (L.b_one) {
-        load4(dst, 0, row0, 0, c * 8);
+    } else if (L.rp == 8) {
+        // an expert's rows are 16 bytes and contiguous: eight of them a line
+        load3(dst, 0, row0 >> 3, c * 8);
     } else {
         const int per = L.rp >> 3;
 #pragma unroll 1
@@ -92,13 +92,40 @@ __device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, 
     }
 }
 
-// Descriptor of the 16-column piece k of such a step.
-__device__ __forceinline__ uint64_t b_step_desc(const TcLinear& L, uint32_t base, uint32_t nrow, int k) {
+// Shared-memory descriptors of the four 16-column pieces of a step: fixed bits
+// and the pieces' offsets, worked out once, so that the issuing thread adds the
+// stage's address and nothing else (it has 512 clocks a step in the pair kernel).
+struct StepDesc {
+    uint64_t fixed;
+    uint32_t off[4];   // in 16-byte units
+    __device__ __forceinline__ uint64_t at(uint32_t base, int k) const {
+        return fixed | (uint64_t)(((base >> 4) + off[k]) & 0x3FFFu);
+    }
+};
+
+// Rows of 64 columns, 128-byte swizzle (W, x, V).
+__device__ __forceinline__ StepDesc row_step_desc() {
+    StepDesc d;
+    d.fixed = sm100::smem_desc(0, 16, 1024, sm100::kSwizzle128B);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d.off[k] = 2u * k;
+    return d;
+}
+
+// A step of the stacked B as load_b_step leaves it.
+__device__ __forceinline__ StepDesc b_step_desc(const TcLinear& L, uint32_t nrow) {
     using namespace sm100;
-    if (!L.b_swizzled) return smem_desc(base + 32u * nrow * k, 16u * nrow, 128, kSwizzleNone);
-    const uint32_t sub = (16u * k) / (uint32_t)L.rp, in = (16u * k) % (uint32_t)L.rp;
-    return smem_desc(base + sub * 2u * nrow * L.rp + in * 2u, 16, 16u * L.rp,
-                     L.rp == 16 ? kSwizzle32B : L.rp == 32 ? kSwizzle64B : kSwizzle128B);
+    StepDesc d;
+    const uint32_t rp = (uint32_t)L.rp;
+    d.fixed = !L.b_swizzled ? smem_desc(0, 16u * nrow, 128, kSwizzleNone)
+                            : smem_desc(0, 16, 16u * rp,
+                                        rp == 16 ? kSwizzle32B : rp == 32 ? kSwizzle64B : kSwizzle128B);
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t sub = (16u * k) / rp, in = (16u * k) % rp;
+        d.off[k] = (L.b_swizzled ? sub * 2u * nrow * rp + in * 2u : 32u * nrow * k) >> 4;
+    }
+    return d;
 }
 
 // The gate of expert e for token t times s: the sum over the record's slots
@@ -176,7 +203,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     uint64_t* acc_full = empty + C::kStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (MODE == kDown) pdl_launch_dependents();
     const int q = (int)(blockIdx.x % (unsigned)S);
@@ -190,7 +217,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);     // one arrival, with its bytes, from each loading warp
             mbar_init(&empty[i], 1);
         }
         mbar_init(acc_full, 1);
@@ -210,66 +237,80 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
         atomicOr(L.p.status, ADAFUSE_STATUS_TIMEOUT);
     };
 
-    if (warp == 4) {
+    if (warp == 4 || warp == 6) {
+        // two warps, since one thread's TMA operations start about 120 clocks
+        // apart: x and V (warp 4), W and B (warp 6)
         if (lane == 0) {
+            const bool left = warp == 4;
             bool waited = false;
             int st = 0;
             uint32_t ph = 0;
 #pragma unroll 1
             for (int i = k0; i < k1; ++i) {
                 if (!wait_phase(&empty[st], ph ^ 1, abort_flag)) { fail(); break; }
-                uint8_t* w_dst = ring + (size_t)st * C::kStageBytes;
-                uint8_t* x_dst = w_dst + C::kWBytes;
+                uint8_t* dst = ring + (size_t)st * C::kStageBytes + (left ? C::kWBytes : 0u);
                 uint64_t* bar = &full[st];
-                mbar_arrive_expect_tx(bar, C::kStageBytes);
-                if (i < L.xsteps) {
-                    tma_load_2d(w_dst, &map_w, i * 64, row0, bar);
-                    tma_load_2d(x_dst, &map_x, i * 64, (int)tok0, bar);
+                const int vi = i - L.xsteps;
+                if (left && vi >= 0 && !waited) {
+                    pdl_wait();   // V is written by the launch before
+                    waited = true;
+                }
+                mbar_arrive_expect_tx(bar, left ? C::kXBytes : C::kWBytes);
+                if (vi < 0) {
+                    if (left)
+                        tma_load_2d(dst, &map_x, i * 64, (int)tok0, bar);
+                    else
+                        tma_load_2d(dst, &map_w, i * 64, row0, bar);
+                } else if (left) {
+                    tma_load_3d(dst, &map_v, (vi % L.bsteps) * 64, (int)tok0, vi / L.bsteps, bar);
                 } else {
-                    const int vi = i - L.xsteps;
-                    load_b_step(L, vi % L.bsteps, row0, 128, w_dst,
+                    load_b_step(L, vi % L.bsteps, row0, 128, dst,
                                 [&](void* d, int a, int b, int c) { tma_load_3d(d, &map_b, a, b, c, bar); },
                                 [&](void* d, int a, int b, int c, int e) {
                                     tma_load_4d(d, &map_b, a, b, c, e, bar);
                                 });
-                    if (!waited) {
-                        pdl_wait();   // V is written by the launch before
-                        waited = true;
-                    }
-                    tma_load_3d(x_dst, &map_v, (vi % L.bsteps) * 64, (int)tok0, vi / L.bsteps, bar);
                 }
                 if (++st == C::kStages) { st = 0; ph ^= 1; }
             }
         }
         __syncwarp();
     } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = instr_desc_bf16(128, TN, 0);
-            int st = 0, acc = -1;
-            uint32_t ph = 0;
-            bool ok = true;
+        // the whole warp walks the steps, so that descriptors are warp-uniform,
+        // and one elected lane issues
+        constexpr uint32_t idesc = instr_desc_bf16(128, TN, 0);
+        const StepDesc rows = row_step_desc(), stacked = b_step_desc(L, 128);
+        const uint32_t ring_s = smem_u32(ring);
+        int st = 0, acc = -1, next = 0;   // accumulator acc takes the steps before `next`
+        uint32_t ph = 0;
+        bool ok = true;
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                if (!wait_phase(&full[st], ph, abort_flag)) { fail(); ok = false; break; }
-                const int a = (int)((int64_t)i * naccs / n);   // accumulator a sums a run of steps
-                const bool first = a != acc;
-                acc = a;
-                const uint32_t w_s = smem_u32(ring + (size_t)st * C::kStageBytes);
-                const uint32_t x_s = w_s + C::kWBytes;
-                const bool adapters = k0 + i >= L.xsteps;
+        for (int i = 0; i < n; ++i) {
+            ok = __all_sync(0xffffffffu, wait_phase(&full[st], ph, abort_flag));
+            if (!ok) break;
+            const bool first = i == next;
+            if (first) {
+                ++acc;
+                next = (acc + 1) * n / naccs;
+            }
+            const uint32_t w_s = ring_s + (uint32_t)st * C::kStageBytes, x_s = w_s + C::kWBytes;
+            const uint32_t d = tmem + (uint32_t)(acc * TN);
+            if (elect_one()) {
+                if (k0 + i < L.xsteps) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t da = adapters ? b_step_desc(L, w_s, 128, k)
-                                                 : smem_desc(w_s + 32u * k, 16, 1024, kSwizzle128B);
-                    const uint64_t db = smem_desc(x_s + 32u * k, 16, 1024, kSwizzle128B);
-                    tc_mma_f16(tmem + (uint32_t)(a * TN), da, db, idesc, !(first && k == 0));
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f16(d, rows.at(w_s, k), rows.at(x_s, k), idesc, !(first && k == 0));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f16(d, stacked.at(w_s, k), rows.at(x_s, k), idesc, !(first && k == 0));
                 }
                 tc_commit(&empty[st]);
-                if (++st == C::kStages) { st = 0; ph ^= 1; }
+                if (i == n - 1) tc_commit(acc_full);
             }
-            if (ok) tc_commit(acc_full);
+            __syncwarp();
+            if (++st == C::kStages) { st = 0; ph ^= 1; }
         }
-        __syncwarp();
+        if (!ok) fail();
     }
 
     // ---- the CTA's partial tile into shared memory: part[token][128 rows]
