@@ -102,22 +102,29 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int f32, flo
     }
 }
 
-// N consecutive columns of y for token t from o (multiples of 8; columns from
-// p.out on are left out): the factor and the residual as 16-byte vectors,
-// requested before the activation, one rounding, 16-byte stores.
+// The factor and the residual of N consecutive columns from o for token t, as
+// 16-byte vectors (columns from p.out on are left out; o and N multiples of 8).
 template <int N>
-__device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, int o, float (&v)[N]) {
-    float m[N], r[N];
-    if (p.mul != nullptr) {
+struct SideCols {
+    float mul[N], res[N];
+    __device__ __forceinline__ void load(const LinearParams& p, int64_t t, int o) {
+        if (p.mul != nullptr) {
 #pragma unroll
-        for (int j = 0; j < N; j += 8)
-            if (o + j < p.out) load8(p.mul, t * p.ldmul + o + j, p.f32, &m[j]);
-    }
-    if (p.res != nullptr) {
+            for (int j = 0; j < N; j += 8)
+                if (o + j < p.out) load8(p.mul, t * p.ldmul + o + j, p.f32, &mul[j]);
+        }
+        if (p.res != nullptr) {
 #pragma unroll
-        for (int j = 0; j < N; j += 8)
-            if (o + j < p.out) load8(p.res, t * p.ldres + o + j, p.f32, &r[j]);
+            for (int j = 0; j < N; j += 8)
+                if (o + j < p.out) load8(p.res, t * p.ldres + o + j, p.f32, &res[j]);
+        }
     }
+};
+
+// Those columns of y from the finished product v: one rounding, 16-byte stores.
+template <int N>
+__device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, int o, float (&v)[N],
+                                            const SideCols<N>& side) {
     if (p.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -126,11 +133,11 @@ __device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, in
     apply_act(v, p.act);
     if (p.mul != nullptr) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= m[i];
+        for (int i = 0; i < N; ++i) v[i] *= side.mul[i];
     }
     if (p.res != nullptr) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += r[i];
+        for (int i = 0; i < N; ++i) v[i] += side.res[i];
     }
     if (p.f32) {
         float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.y) + t * p.ldy + o);

@@ -118,10 +118,13 @@ cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t sme
 }
 
 // Cluster size of the skinny kernel: the contraction is split while the grid
-// stays within two CTAs an SM and every CTA keeps at least four steps.
+// stays within one CTA an SM and every CTA keeps at least four steps.  Measured
+// at T = 61 (4096 -> 1024, 4096 -> 4096, 11008 -> 4096, 4096 -> 11008): 10.2,
+// 13.1, 21.6 and 21.5 us at the sizes this takes (8, 4, 4, 1: 10.5, 13.1, 21.6,
+// 21.5), up to twice that at the others.
 inline int skinny_split(int64_t tiles, int nsteps, int sm_count) {
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= 2 * (int64_t)sm_count && nsteps / (S * 2) >= 4) S *= 2;
+    while (S < 8 && tiles * S * 2 <= sm_count && nsteps / (S * 2) >= 4) S *= 2;
     return S;
 }
 
@@ -137,10 +140,11 @@ cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMa
     const int64_t tiles = ceil_div(L.rows, 128) * L.tok_tiles;
     const int S = skinny_split(tiles, L.xsteps + L.vsteps, ctx->sm_count);
     if (tiles * S > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const int stages = C::stages(tiles * S <= ctx->sm_count ? 1 : 2);
     auto kernel = linear_skinny_kernel<TN, MODE>;
-    ensure_smem_attr(kernel, C::kSmemBytes, ctx->device);
-    return launch_clusters(kernel, tiles * S, kSkinnyThreads, C::kSmemBytes, S, overlap, s, L, map_w, map_x,
-                           map_b, map_v, S);
+    ensure_smem_attr(kernel, C::smem_bytes(C::stages(1)), ctx->device);
+    return launch_clusters(kernel, tiles * S, kSkinnyThreads, C::smem_bytes(stages), S, overlap, s, L, map_w,
+                           map_x, map_b, map_v, S, stages);
 }
 
 template <int MODE>
@@ -180,9 +184,44 @@ cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, fl
                                   W, rows, u, S);
 }
 
-template <int BN, bool CHUNKED>
+// Estimated time (us) of a 64-column step of a 256 x BN tile on a CTA pair
+// (measured 0.18 at BN = 128 to 0.34 at 256 with every SM busy).
+inline double pair_step_us(int bn) { return 0.02 + 0.00125 * bn; }
+
+// Tile width of the pair kernel: the multiple of 16 in [128, 256] with the least
+// estimated time for the longest pair's share, the narrower among equals (their
+// tiles finish sooner).  *us: that estimate for nsteps.
+inline int pair_width(int64_t tok_tiles, int out, int64_t pairs, int nsteps, double* us) {
+    int best = kPairMaxCols;
+    double least = 1e300;
+    for (int bn = kPairMaxCols; bn >= 128; bn -= 16) {
+        const double t = (double)ceil_div(tok_tiles * ceil_div(out, bn), pairs) * pair_step_us(bn);
+        if (t <= least) { least = t; best = bn; }
+    }
+    *us = 6.0 + least * nsteps;
+    return best;
+}
+
+// More than 128 tokens: the skinny kernel (tiles of 128 x 128, contraction
+// split) where its estimate is below the pair kernel's, that is where the pair
+// kernel has too few tiles to occupy the SMs.  Measured at T = 333 4096 -> 1024:
+// 13.8 against 17.6 us; T = 1037 4096 -> 1024: 15.4 against 17.4 us.
+inline bool pair_is_faster(const TcLinear& L, int sm_count) {
+    const int nsteps = L.xsteps + L.vsteps;
+    double pair_us;
+    pair_width(ceil_div(L.p.T, kPairTokens), L.p.out, sm_count / 2, nsteps, &pair_us);
+    const int64_t tiles = ceil_div(L.p.out, 128) * ceil_div(L.p.T, 128);
+    const int S = skinny_split(tiles, nsteps, sm_count);
+    const double skinny_us = 7.0 + (double)(ceil_div(tiles * S, sm_count) * ceil_div(nsteps, S)) * 0.19;
+    return pair_us <= skinny_us;
+}
+
+template <bool CHUNKED>
 cudaError_t launch_pair(TcLinear L, bool overlap, const adafuse_ctx* ctx, cudaStream_t s) {
-    using C = PairConfig<BN>;
+    L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
+    const int64_t most = ctx->sm_count / 2;
+    double us;
+    const int BN = pair_width(L.tok_tiles, L.p.out, most, L.xsteps + L.vsteps, &us);
     CUtensorMap map_w, map_x, map_b, map_v;
     std::memset(&map_b, 0, sizeof map_b);
     std::memset(&map_v, 0, sizeof map_v);
@@ -191,13 +230,11 @@ cudaError_t launch_pair(TcLinear L, bool overlap, const adafuse_ctx* ctx, cudaSt
         return cudaErrorInvalidValue;
     if (L.vsteps > 0 && (!encode_b(&map_b, L, BN / 2) || !encode_v(&map_v, L, 128)))
         return cudaErrorInvalidValue;
-    L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
     const int64_t tiles = L.tok_tiles * ceil_div(L.p.out, BN);
-    auto kernel = linear_pair_kernel<BN, CHUNKED>;
-    ensure_smem_attr(kernel, C::kSmemBytes, ctx->device);
-    const int64_t pairs = std::min<int64_t>(tiles, ctx->sm_count / 2);
-    return launch_clusters(kernel, 2 * pairs, kPairThreads, C::kSmemBytes, 2, overlap, s, L, map_w, map_x,
-                           map_b, map_v);
+    auto kernel = linear_pair_kernel<CHUNKED>;
+    ensure_smem_attr(kernel, kPairSmemBytes, ctx->device);
+    return launch_clusters(kernel, 2 * std::min(tiles, most), kPairThreads, kPairSmemBytes, 2, overlap, s, L,
+                           map_w, map_x, map_b, map_v, BN);
 }
 
 // y of one product; L carries V's geometry when the adapters are part of it.
@@ -205,8 +242,8 @@ inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream
     L.rows = L.p.out;
     L.xsteps = (int)ceil_div(L.p.in, 64);
     const bool overlap = L.vsteps > 0;
-    if (L.p.T > 128)
-        return L.p.f32 ? launch_pair<256, true>(L, overlap, ctx, s) : launch_pair<256, false>(L, overlap, ctx, s);
+    if (L.p.T > 128 && pair_is_faster(L, ctx->sm_count))
+        return L.p.f32 ? launch_pair<true>(L, overlap, ctx, s) : launch_pair<false>(L, overlap, ctx, s);
     CUtensorMap map_w, map_b;
     std::memset(&map_b, 0, sizeof map_b);
     if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;

@@ -10,10 +10,12 @@
 // slice of the tile over the S partials in rank order (no atomics, so the same
 // bits every time), applies the epilogue and stores it.
 //
-// Tensor-core accumulators drop low bits on every 16-deep step (measured: 4e-6
-// of the result after 4096 products, 1.2e-5 after 11008).  A CTA therefore
-// spreads its part over several TMEM accumulators, each summing a run of it,
-// and joins them in registers with fp32 additions.
+// A CTA spreads its part over several TMEM accumulators, one 16-deep piece after
+// the other, and joins them in registers with fp32 additions, for two reasons:
+// successive MMAs on one accumulator wait for each other (about 130 clocks,
+// whatever the width: a 64-column step took 0.28 us on one), and accumulators
+// drop low bits on every piece (measured: 4e-6 of the result after 4096
+// products, 1.2e-5 after 11008).
 //
 // Routed products append the adapters to the contraction: after the columns of
 // x come those of V [T, E * rp] (every token's gated x A^T, zero for experts it
@@ -45,22 +47,35 @@ struct TcLinear {
     int tok_tiles;     // token tiles
 };
 
-constexpr int kSkinnyThreads = 224;
+constexpr int kSkinnyThreads = 384;
 
-// Wait for the phase with the given parity; gives up after `limit` clocks or
-// once *abort is set.  Bounded by the SM's own clock, read every few polls:
-// the global timer costs enough per read to pace these short waits.
+// Wait, as a whole warp, for the phase with the given parity of the barrier at
+// shared-memory address `bar`; gives up (for all lanes alike) after `limit`
+// clocks or once *abort is set.  Bounded by the SM's own clock, read every few
+// polls: the global timer costs enough per read to pace these short waits.
 constexpr long long kWaitClocks = 2000000000ll;   // about 1 s
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort,
                                            long long limit = kWaitClocks) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (sm100::mbar_try_wait(bar, parity)) return true;
-        if (*abort || clock64() - t0 > limit) return false;
+    uint32_t polls = 0;
+    long long t0 = 0;
+    while (!__all_sync(0xffffffffu, try_phase(bar, parity))) {
+        if ((++polls & 15u) != 0) continue;
+        const long long now = clock64();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > limit)) return false;
     }
+    return true;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -71,55 +86,141 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// Loads of one 64-column step of the stacked B for `nrow` (128 or 64) out rows
-// from row0: columns 64 * c .. of the E * rp stacked ones.  Experts past E read
-// as zero.
-template <typename Load3, typename Load4>
-__device__ __forceinline__ void load_b_step(const TcLinear& L, int c, int row0, int nrow, uint8_t* dst,
-                                            Load3&& load3, Load4&& load4) {
+// TMA loads named by shared-memory addresses, in their single-CTA and their
+// CTA-pair form (the pair's completion may be counted in either CTA).
+template <bool PAIR>
+struct Tma {
+    static __device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+        if constexpr (PAIR)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+        else
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+    }
+    static __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                                 uint32_t bar) {
+        if constexpr (PAIR)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+                : "memory");
+        else
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+                : "memory");
+    }
+    static __device__ __forceinline__ void load4(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w,
+                                                 uint32_t bar) {
+        if constexpr (PAIR)
+            asm volatile(
+                "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                : "memory");
+        else
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                : "memory");
+    }
+    // arrive on a barrier, announcing `bytes` that will complete on it
+    static __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+        if constexpr (PAIR)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                         : "memory");
+        else
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                         : "memory");
+    }
+};
+
+// Loads of one 64-column step of the stacked B for `nrow` out rows from row0:
+// columns 64 * c .. of the E * rp stacked ones.  Experts past E read as zero.
+template <bool PAIR>
+__device__ __forceinline__ void load_b_step(const TcLinear& L, const CUtensorMap* m, int c, int row0, int nrow,
+                                            uint32_t dst, uint32_t bar) {
     if (L.b_swizzled) {
-        load3(dst, 0, row0, c * (64 / L.rp));
+        Tma<PAIR>::load3(dst, m, 0, row0, c * (64 / L.rp), bar);
     } else if (L.rp == 8) {
         // an expert's rows are 16 bytes and contiguous: eight of them a line
-        load3(dst, 0, row0 >> 3, c * 8);
+        Tma<PAIR>::load3(dst, m, 0, row0 >> 3, c * 8, bar);
     } else {
         const int per = L.rp >> 3;
 #pragma unroll 1
         for (int j = 0; j < 8; ++j) {
             const int grp = c * 8 + j;
-            load4(dst + j * 16 * nrow, 0, row0, grp % per, grp / per);
+            Tma<PAIR>::load4(dst + (uint32_t)(j * 16 * nrow), m, 0, row0, grp % per, grp / per, bar);
         }
     }
 }
 
-// Shared-memory descriptors of the four 16-column pieces of a step: fixed bits
-// and the pieces' offsets, worked out once, so that the issuing thread adds the
-// stage's address and nothing else (it has 512 clocks a step in the pair kernel).
-struct StepDesc {
-    uint64_t fixed;
-    uint32_t off[4];   // in 16-byte units
-    __device__ __forceinline__ uint64_t at(uint32_t base, int k) const {
-        return fixed | (uint64_t)(((base >> 4) + off[k]) & 0x3FFFu);
+// One loading warp's share of an output tile, steps [k0, k1): x and V (LEFT) or
+// W and the stacked B, into slot `dst0 + stage * stage_bytes` of each stage.
+// The whole warp walks the steps and an elected lane issues, so that addresses
+// and coordinates stay in uniform registers: walked by one lane alone a step
+// took about 530 clocks.  Returns false when a wait gave up.
+template <bool PAIR, bool LEFT>
+__device__ __forceinline__ bool load_steps(const TcLinear& L, const CUtensorMap* map_k, const CUtensorMap* map_a,
+                                           int k0, int k1, int at, int nrow, uint32_t bytes, uint32_t dst0,
+                                           uint32_t stage_bytes, uint32_t empty, uint32_t full0, int stages,
+                                           int& st, uint32_t& ph, bool& waited, volatile int* abort) {
+    const bool lead = sm100::elect_one();
+    const int kx = k1 < L.xsteps ? k1 : L.xsteps;
+#pragma unroll 1
+    for (int i = k0; i < kx; ++i) {
+        if (!wait_phase(empty + 8u * (uint32_t)st, ph ^ 1, abort)) return false;
+        const uint32_t bar = full0 + 8u * (uint32_t)st;
+        if (lead) {
+            Tma<PAIR>::expect(bar, bytes);
+            Tma<PAIR>::load2(dst0 + (uint32_t)st * stage_bytes, map_k, i * 64, at, bar);
+        }
+        if (++st == stages) { st = 0; ph ^= 1; }
     }
+    if (k1 <= L.xsteps) return true;
+    if (LEFT && !waited) {
+        pdl_wait();   // V is written by the launch before
+        waited = true;
+    }
+#pragma unroll 1
+    for (int i = k0 > L.xsteps ? k0 : L.xsteps; i < k1; ++i) {
+        if (!wait_phase(empty + 8u * (uint32_t)st, ph ^ 1, abort)) return false;
+        const uint32_t bar = full0 + 8u * (uint32_t)st, dst = dst0 + (uint32_t)st * stage_bytes;
+        const int vi = i - L.xsteps;
+        if (lead) {
+            Tma<PAIR>::expect(bar, bytes);
+            if constexpr (LEFT)
+                Tma<PAIR>::load3(dst, map_a, (vi % L.bsteps) * 64, at, vi / L.bsteps, bar);
+            else
+                load_b_step<PAIR>(L, map_a, vi % L.bsteps, at, nrow, dst, bar);
+        }
+        if (++st == stages) { st = 0; ph ^= 1; }
+    }
+    return true;
+}
+
+// Shared-memory descriptor of a step's first 16-column piece at address 0, and
+// what to add for the other three; a stage's address is added in 16-byte units.
+struct StepDesc {
+    uint64_t base;
+    uint32_t off[4];
 };
 
 // Rows of 64 columns, 128-byte swizzle (W, x, V).
-__device__ __forceinline__ StepDesc row_step_desc() {
-    StepDesc d;
-    d.fixed = sm100::smem_desc(0, 16, 1024, sm100::kSwizzle128B);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) d.off[k] = 2u * k;
-    return d;
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
+    return sm100::smem_desc(addr, 16, 1024, sm100::kSwizzle128B);
 }
 
 // A step of the stacked B as load_b_step leaves it.
-__device__ __forceinline__ StepDesc b_step_desc(const TcLinear& L, uint32_t nrow) {
+__device__ __forceinline__ StepDesc b_desc(const TcLinear& L, uint32_t addr, uint32_t nrow) {
     using namespace sm100;
     StepDesc d;
     const uint32_t rp = (uint32_t)L.rp;
-    d.fixed = !L.b_swizzled ? smem_desc(0, 16u * nrow, 128, kSwizzleNone)
-                            : smem_desc(0, 16, 16u * rp,
-                                        rp == 16 ? kSwizzle32B : rp == 32 ? kSwizzle64B : kSwizzle128B);
+    d.base = !L.b_swizzled ? smem_desc(addr, 16u * nrow, 128, kSwizzleNone)
+                           : smem_desc(addr, 16, 16u * rp,
+                                       rp == 16 ? kSwizzle32B : rp == 32 ? kSwizzle64B : kSwizzle128B);
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k) {
         const uint32_t sub = (16u * k) / rp, in = (16u * k) % rp;
@@ -177,13 +278,14 @@ struct SkinnyConfig {
     static constexpr uint32_t kWBytes = 128 * 128;          // 128 rows x 64 columns bf16
     static constexpr uint32_t kXBytes = TN * 128;
     static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-    // two CTAs an SM: at most 113 KB each
-    static constexpr int kStages = TN <= 32 ? 5 : TN == 64 ? 4 : 3;
     static constexpr int kAccs = TN == 128 ? 2 : TN == 64 ? 4 : 8;   // TMEM accumulators
-    static constexpr uint32_t kTmemCols = kAccs * TN;                // 128 or 256
-    static constexpr uint32_t kRingBytes = kStages * kStageBytes;
-    static constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * (2 * kStages + 1) + 16;
-    static_assert(TN * 128 * 4 <= kRingBytes, "the partial tile reuses the ring");
+    static constexpr uint32_t kTmemCols = kAccs * TN;                // 128 or 256: two CTAs fit
+    // stages of a launch with `ctas` (1 or 2) CTAs an SM
+    static constexpr int stages(int ctas) {
+        return (int)((ctas == 1 ? 216u * 1024u : 108u * 1024u) / kStageBytes);
+    }
+    static constexpr uint32_t smem_bytes(int stages) { return 1024 + stages * kStageBytes + 8 * (2 * stages + 1) + 16; }
+    static_assert(TN * 128 * 4 <= 3 * kStageBytes, "the partial tile reuses the ring");
     static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 };
 
@@ -192,15 +294,15 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_b,
-                     const __grid_constant__ CUtensorMap map_v, const int S) {
+                     const __grid_constant__ CUtensorMap map_v, const int S, const int stages) {
     using C = SkinnyConfig<TN>;
     using namespace sm100;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRingBytes);
-    uint64_t* empty = full + C::kStages;
-    uint64_t* acc_full = empty + C::kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * C::kStageBytes);
+    uint64_t* empty = full + stages;
+    uint64_t* acc_full = empty + stages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -213,10 +315,10 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     const int nsteps = L.xsteps + L.vsteps;
     const int k0 = (int)((int64_t)q * nsteps / S), k1 = (int)((int64_t)(q + 1) * nsteps / S);
     const int n = k1 - k0;
-    const int naccs = n < C::kAccs ? n : C::kAccs;
+    const int naccs = 4 * n < C::kAccs ? 4 * n : C::kAccs;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(&full[i], 2);     // one arrival, with its bytes, from each loading warp
             mbar_init(&empty[i], 1);
         }
@@ -238,86 +340,77 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     };
 
     if (warp == 4 || warp == 6) {
-        // two warps, since one thread's TMA operations start about 120 clocks
-        // apart: x and V (warp 4), W and B (warp 6)
-        if (lane == 0) {
-            const bool left = warp == 4;
-            bool waited = false;
-            int st = 0;
-            uint32_t ph = 0;
-#pragma unroll 1
-            for (int i = k0; i < k1; ++i) {
-                if (!wait_phase(&empty[st], ph ^ 1, abort_flag)) { fail(); break; }
-                uint8_t* dst = ring + (size_t)st * C::kStageBytes + (left ? C::kWBytes : 0u);
-                uint64_t* bar = &full[st];
-                const int vi = i - L.xsteps;
-                if (left && vi >= 0 && !waited) {
-                    pdl_wait();   // V is written by the launch before
-                    waited = true;
-                }
-                mbar_arrive_expect_tx(bar, left ? C::kXBytes : C::kWBytes);
-                if (vi < 0) {
-                    if (left)
-                        tma_load_2d(dst, &map_x, i * 64, (int)tok0, bar);
-                    else
-                        tma_load_2d(dst, &map_w, i * 64, row0, bar);
-                } else if (left) {
-                    tma_load_3d(dst, &map_v, (vi % L.bsteps) * 64, (int)tok0, vi / L.bsteps, bar);
-                } else {
-                    load_b_step(L, vi % L.bsteps, row0, 128, dst,
-                                [&](void* d, int a, int b, int c) { tma_load_3d(d, &map_b, a, b, c, bar); },
-                                [&](void* d, int a, int b, int c, int e) {
-                                    tma_load_4d(d, &map_b, a, b, c, e, bar);
-                                });
-                }
-                if (++st == C::kStages) { st = 0; ph ^= 1; }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 5) {
-        // the whole warp walks the steps, so that descriptors are warp-uniform,
-        // and one elected lane issues
-        constexpr uint32_t idesc = instr_desc_bf16(128, TN, 0);
-        const StepDesc rows = row_step_desc(), stacked = b_step_desc(L, 128);
-        const uint32_t ring_s = smem_u32(ring);
-        int st = 0, acc = -1, next = 0;   // accumulator acc takes the steps before `next`
+        // two loading warps: one thread's TMA operations start about 120 clocks apart
+        int st = 0;
         uint32_t ph = 0;
+        bool waited = false;
+        const uint32_t ring_s = smem_u32(ring), full_s = smem_u32(full);
+        const bool ok =
+            warp == 4 ? load_steps<false, true>(L, &map_x, &map_v, k0, k1, (int)tok0, 0, C::kXBytes,
+                                                ring_s + C::kWBytes, C::kStageBytes, smem_u32(empty), full_s, stages, st,
+                                                ph, waited, abort_flag)
+                      : load_steps<false, false>(L, &map_w, &map_b, k0, k1, row0, 128, C::kWBytes, ring_s,
+                                                 C::kStageBytes, smem_u32(empty), full_s, stages, st, ph, waited,
+                                                 abort_flag);
+        if (!ok) fail();
+    } else if (warp == 5) {
+        // The whole warp walks the steps with the fewest possible operations
+        // between the MMAs, and one elected lane issues: descriptors stay in
+        // uniform registers and a step takes about 200 clocks instead of 520.
+        constexpr uint32_t idesc = instr_desc_bf16(128, TN, 0);
+        const uint32_t ring_s = smem_u32(ring), full_s = smem_u32(full), empty_s = smem_u32(empty);
+        const uint64_t dw = row_desc(ring_s), dx = row_desc(ring_s + C::kWBytes);
+        const StepDesc db = b_desc(L, ring_s, 128);
+        int st = 0, i = 0;
+        uint32_t ph = 0, off = 0;       // off: the stage's offset in 16-byte units
         bool ok = true;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            ok = __all_sync(0xffffffffu, wait_phase(&full[st], ph, abort_flag));
-            if (!ok) break;
-            const bool first = i == next;
-            if (first) {
-                ++acc;
-                next = (acc + 1) * n / naccs;
-            }
-            const uint32_t w_s = ring_s + (uint32_t)st * C::kStageBytes, x_s = w_s + C::kWBytes;
-            const uint32_t d = tmem + (uint32_t)(acc * TN);
-            if (elect_one()) {
-                if (k0 + i < L.xsteps) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f16(d, rows.at(w_s, k), rows.at(x_s, k), idesc, !(first && k == 0));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f16(d, stacked.at(w_s, k), rows.at(x_s, k), idesc, !(first && k == 0));
-                }
-                tc_commit(&empty[st]);
-                if (i == n - 1) tc_commit(acc_full);
-            }
+        // successive MMAs go to different accumulators (see the file's head)
+        auto acc_of = [&](int k) {
+            return tmem + (uint32_t)((k & (C::kAccs >= 4 ? 3 : 1)) * TN) +
+                   (C::kAccs == 8 && (i & 1) ? 4u * TN : 0u);
+        };
+        auto fresh = [&](int k) { return C::kAccs == 8 ? i < 2 : C::kAccs == 4 ? i == 0 : i == 0 && k < 2; };
+        auto next_stage = [&]() {
             __syncwarp();
-            if (++st == C::kStages) { st = 0; ph ^= 1; }
+            ++i;
+            ++st;
+            off += C::kStageBytes / 16;
+            if (st == stages) { st = 0; off = 0; ph ^= 1; }
+        };
+        const int nx = (k1 < L.xsteps ? k1 : L.xsteps) - k0;   // steps of x and W (<= 0: none)
+#pragma unroll 1
+        while (i < nx) {
+            ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
+            if (!ok) break;
+            const uint64_t a = dw + off, b = dx + off;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + 2 * k, b + 2 * k, idesc, !fresh(k));
+                tc_commit_addr(empty_s + 8u * (uint32_t)st);
+            }
+            next_stage();
         }
+#pragma unroll 1
+        while (ok && i < n) {
+            ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
+            if (!ok) break;
+            const uint64_t a = db.base + off, b = dx + off;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + db.off[k], b + 2 * k, idesc, !fresh(k));
+                tc_commit_addr(empty_s + 8u * (uint32_t)st);
+            }
+            next_stage();
+        }
+        if (ok && elect_one()) tc_commit(acc_full);
+        __syncwarp();
         if (!ok) fail();
     }
 
     // ---- the CTA's partial tile into shared memory: part[token][128 rows]
     float* part = reinterpret_cast<float*>(ring);
     if (warp < 4) {
-        const bool ok = wait_phase(acc_full, 0, abort_flag, 4 * kWaitClocks);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (wait_phase(smem_u32(acc_full), 0, abort_flag, 4 * kWaitClocks)) {
             tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
             constexpr int kCols = TN < 32 ? 16 : 32;
@@ -362,36 +455,45 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             fail();
         }
     }
+    // ---- this CTA's slice of the tile: sum over the cluster, epilogue, store
+    const int ntok = (int)(L.p.T - tok0 < TN ? L.p.T - tok0 : TN);
+    const int nrow = L.rows - row0 < 128 ? L.rows - row0 : 128;
+    const int groups = ntok * 16;
+    const int g0 = (int)((int64_t)q * groups / S), g1 = (int)((int64_t)(q + 1) * groups / S);
+    SideCols<8> side;
+    // what does not depend on the sums is requested before they are complete
+    auto request = [&](int gi) {
+        if (MODE == kProduct && gi < g1 && (gi & 15) * 8 < nrow)
+            side.load(L.p, tok0 + (gi >> 4), row0 + (gi & 15) * 8);
+    };
+    request(g0 + (int)threadIdx.x);
     __syncthreads();
     if (S > 1) cluster_sync();
-
-    // ---- this CTA's slice of the tile: sum over the cluster, epilogue, store
     if (!*abort_flag) {
-        const int ntok = (int)(L.p.T - tok0 < TN ? L.p.T - tok0 : TN);
-        const int nrow = L.rows - row0 < 128 ? L.rows - row0 : 128;
-        const int groups = ntok * 16;
-        const int g0 = (int)((int64_t)q * groups / S), g1 = (int)((int64_t)(q + 1) * groups / S);
         const uint32_t part_s = smem_u32(part);
         int bad = 0;
 #pragma unroll 1
         for (int gi = g0 + (int)threadIdx.x; gi < g1; gi += kSkinnyThreads) {
             const int tok = gi >> 4, r8 = (gi & 15) * 8;
-            if (r8 >= nrow) continue;
-            float v[8];
+            if (r8 < nrow) {
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-            const uint32_t off = part_s + (uint32_t)(tok * 128 + r8) * 4u;
-            for (int c = 0; c < S; ++c) {
-                uint32_t a = off;
-                if (S > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(off), "r"(c));
-                const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
-                v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-                v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                const uint32_t off = part_s + (uint32_t)(tok * 128 + r8) * 4u;
+#pragma unroll 4
+                for (int c = 0; c < S; ++c) {
+                    uint32_t a = off;
+                    if (S > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(off), "r"(c));
+                    const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
+                    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+                    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                }
+                if constexpr (MODE == kDown)
+                    finish_down8(L, tok0 + tok, row0 + r8, v, bad);
+                else
+                    finish_cols(L.p, tok0 + tok, row0 + r8, v, side);
             }
-            if constexpr (MODE == kDown)
-                finish_down8(L, tok0 + tok, row0 + r8, v, bad);
-            else
-                finish_cols<8>(L.p, tok0 + tok, row0 + r8, v);
+            request(gi + kSkinnyThreads);
         }
         if (MODE == kDown && bad != 0) atomicOr(L.p.status, bad);
     } else {
