@@ -386,12 +386,19 @@ def _need(t, dtype: str, what: str) -> None:
         raise ValueError(f"{what}: the last dimension must be contiguous")
 
 
-def _row_stride(t) -> int:
-    """Elements between row starts (a row's length when there is one row or none)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-_DTYPES = {"torch.bfloat16": ADAFUSE_DTYPE_BF16, "torch.float32": ADAFUSE_DTYPE_F32}
+def _rows(t, dtype, T: int, n: int, what: str):
+    """(address, elements between row starts) of a [T, n] device tensor whose
+    rows are contiguous.  On the decode path: few attribute reads."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != (T, n):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(T, n)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not on a CUDA device")
+    ld, unit = t.stride()
+    if unit != 1 and n > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), ld if T > 1 else n
 
 
 class Switcher:
@@ -411,6 +418,10 @@ class Switcher:
             name = names[i % n_targets] if names else f"t{i % n_targets}"
             ts.append((name, w.shape[0], w.shape[1], w.data_ptr(), a.data_ptr(), b.data_ptr()))
         self._tensors = (list(W), list(A), list(B))
+        self._shapes = [tuple(w.shape) for w in W]
+        import torch
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._types = {torch.bfloat16: ADAFUSE_DTYPE_BF16, torch.float32: ADAFUSE_DTYPE_F32}
         self.desc = make_desc(n_layers, n_targets, n_experts, rank, alpha, ts)
         self.n_layers = n_layers
         self.ctx = adafuse_create(self.desc, device)
@@ -482,49 +493,44 @@ class Switcher:
         """One decision per row of h [T, d] (bf16 or fp32) into ``routes``, an
         int32 [T, 2 * slots] buffer of 2, 4 or 8 slots a record."""
         T, d = h.shape
-        dtype = _DTYPES.get(str(h.dtype))
-        if dtype is None:
+        types = self._types
+        h_dtype = types.get(h.dtype)
+        if h_dtype is None:
             raise TypeError(f"h: dtype {h.dtype}, expected bfloat16 or float32")
-        _need(h, str(h.dtype)[6:], "h")
-        _need(Wr, "float32", "Wr")
-        _need(routes, "int32", "routes")
+        hp, ldh = _rows(h, h.dtype, T, d, "h")
         E = self.desc.n_experts
-        if tuple(Wr.shape) != (d, E) or not Wr.is_contiguous():
-            raise ValueError(f"Wr: shape {tuple(Wr.shape)}, expected a contiguous {(d, E)}")
+        wp, ldw = _rows(Wr, self._f32, d, E, "Wr")
+        if ldw != E:
+            raise ValueError("Wr: rows must be contiguous")
         if gating._keep is not None and gating._keep.numel() != E:
             raise ValueError(f"bias: {gating._keep.numel()} values for {E} experts")
-        if routes.shape[0] != T or not routes.is_contiguous():
+        slots = routes.shape[-1] // 2
+        rp, ldr = _rows(routes, self._i32, T, 2 * slots, "routes")
+        if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of h")
-        adafuse_route_experts(self.ctx, h.data_ptr(), dtype, T, d, _row_stride(h), Wr.data_ptr(),
-                              gating, routes.shape[1] // 2, routes.data_ptr(), stream)
+        adafuse_route_experts(self.ctx, hp, h_dtype, T, d, ldh, wp, gating, slots, rp, stream)
 
     def _linear_args(self, layer, target, x, y, bias, activation, mul, residual, base):
-        n_targets = self.desc.n_targets
-        if not (0 <= layer < self.n_layers and 0 <= target < n_targets):
+        if not (0 <= layer < self.n_layers and 0 <= target < self.desc.n_targets):
             raise ValueError(f"no weight ({layer}, {target})")
-        out, inn = self._tensors[0][layer * n_targets + target].shape
+        out, inn = self._shapes[layer * self.desc.n_targets + target]
         T = x.shape[0]
-        io = _DTYPES.get(str(y.dtype))
+        dtype = y.dtype
+        io = self._types.get(dtype)
         if io is None:
-            raise TypeError(f"y: dtype {y.dtype}, expected bfloat16 or float32")
-        _need(x, "bfloat16", "x")
-        if tuple(x.shape) != (T, inn):
-            raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, inn)}")
-        for name, t in (("y", y), ("mul", mul), ("residual", residual)):
-            if t is not None:
-                _need(t, str(y.dtype)[6:], name)
-                if tuple(t.shape) != (T, out):
-                    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, out)}")
+            raise TypeError(f"y: dtype {dtype}, expected bfloat16 or float32")
+        xp, ldx = _rows(x, self._bf16, T, inn, "x")
+        yp, ldy = _rows(y, dtype, T, out, "y")
+        mp, ldm = (None, 0) if mul is None else _rows(mul, dtype, T, out, "mul")
+        rp, ldr = (None, 0) if residual is None else _rows(residual, dtype, T, out, "residual")
+        bp = None
         if bias is not None:
-            _need(bias, "float32", "bias")
-            if tuple(bias.shape) != (out,):
+            if bias.shape != (out,):
                 raise ValueError(f"bias: shape {tuple(bias.shape)}, expected {(out,)}")
-        p = lambda t: None if t is None else t.data_ptr()
-        ld = lambda t: 0 if t is None else _row_stride(t)
-        return LinearArgs(int(layer), int(target),
-                          ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT, int(activation),
-                          io, T, p(x), ld(x), p(bias), p(mul), ld(mul), p(residual), ld(residual),
-                          p(y), ld(y))
+            _need(bias, "float32", "bias")
+            bp = bias.data_ptr()
+        return LinearArgs(layer, target, ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT,
+                          activation, io, T, xp, ldx, bp, mp, ldm, rp, ldr, yp, ldy)
 
     def linear(self, layer: int, target: int, x, y, bias=None, activation: int = ADAFUSE_ACT_NONE,
                mul=None, residual=None, base: bool = False, stream: int = 0) -> None:
@@ -545,12 +551,13 @@ class Switcher:
         [T, 2 * slots]); workspace: a device uint8 tensor of at least
         linear_workspace() bytes that no overlapping call uses."""
         a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
-        _need(routes, "int32", "routes")
-        if routes.shape[0] != x.shape[0] or not routes.is_contiguous():
+        slots = routes.shape[-1] // 2
+        rp, ldr = _rows(routes, self._i32, a.T, 2 * slots, "routes")
+        if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of x")
-        adafuse_linear_routed(self.ctx, a, routes.data_ptr(), routes.shape[1] // 2,
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              stream)
+        if not workspace.is_cuda:
+            raise ValueError("workspace: not on a CUDA device")
+        adafuse_linear_routed(self.ctx, a, rp, slots, workspace.data_ptr(), workspace.nbytes, stream)
 
     def set_kernel(self, kernel: int) -> None:
         adafuse_set_switch_kernel(self.ctx, kernel)

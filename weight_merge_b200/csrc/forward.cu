@@ -74,6 +74,42 @@ int linear_params(const adafuse_ctx* ctx, const adafuse_linear_args* a, LinearPa
     return ADAFUSE_OK;
 }
 
+// One launch of the router: 32 tokens a CTA, their columns shared by a cluster
+// of up to 8 CTAs while that keeps the grid resident at once.
+template <int EMAX, bool VEC, typename H>
+cudaError_t launch_route_as(const H* h, int64_t T, int64_t d, int64_t ldh, const float* Wr, const GateParams& g,
+                            int32_t* route, const adafuse_ctx* ctx, cudaStream_t s) {
+    const int64_t groups = ceil_div(T, kRouteTokens), chunks = ceil_div(d, kRouteDepth);
+    int C = 1;
+    const int64_t most = (EMAX <= 16 ? 2 : 1) * (int64_t)ctx->sm_count;   // resident CTAs
+    while (C < 8 && groups * C * 2 <= most && chunks >= C * 2) C *= 2;
+    if (groups * C > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const size_t smem = std::max<size_t>(kRouteStages * route_stage_bytes<H>(g.E), route_tail_bytes<EMAX>());
+    auto kernel = route_experts_kernel<EMAX, VEC, H>;
+    ensure_smem_attr(kernel, smem, ctx->device);
+    const int h_piece = ldh * (int64_t)sizeof(H) % 16 == 0 ? 16 : 8;
+    const int w_piece = (reinterpret_cast<uintptr_t>(Wr) & 15u) == 0 ? 16 : 4;
+    return launch_clusters(kernel, groups * C, kRouteThreads, smem, C, false, s, h, T, d, ldh, Wr, g, route, C,
+                           h_piece, w_piece);
+}
+
+template <typename H>
+cudaError_t launch_route(const H* h, int64_t T, int64_t d, int64_t ldh, const float* Wr, const GateParams& g,
+                         int32_t* route, const adafuse_ctx* ctx, cudaStream_t s) {
+    const int E = g.E;
+    if (E <= 8)
+        return E % 2 == 0 ? launch_route_as<8, true>(h, T, d, ldh, Wr, g, route, ctx, s)
+                          : launch_route_as<8, false>(h, T, d, ldh, Wr, g, route, ctx, s);
+    if (E <= 16)
+        return E % 4 == 0 ? launch_route_as<16, true>(h, T, d, ldh, Wr, g, route, ctx, s)
+                          : launch_route_as<16, false>(h, T, d, ldh, Wr, g, route, ctx, s);
+    if (E <= 32)
+        return E % 4 == 0 ? launch_route_as<32, true>(h, T, d, ldh, Wr, g, route, ctx, s)
+                          : launch_route_as<32, false>(h, T, d, ldh, Wr, g, route, ctx, s);
+    return E % 4 == 0 ? launch_route_as<64, true>(h, T, d, ldh, Wr, g, route, ctx, s)
+                      : launch_route_as<64, false>(h, T, d, ldh, Wr, g, route, ctx, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -104,14 +140,10 @@ int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int6
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const GateParams g{q.score, q.k, q.n_groups, q.top_groups, q.group_top, q.renorm != 0,
                        q.scale, q.bias, E, slots};
-    const unsigned grid = (unsigned)std::min<int64_t>(T, (int64_t)ctx->sm_count * 8);
     int32_t* rt = static_cast<int32_t*>(route);
-    if (h_dtype == ADAFUSE_DTYPE_F32)
-        route_experts_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(h), T, d, ldh, Wr, g, rt);
-    else
-        route_experts_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(h), T, d, ldh, Wr,
-                                                  g, rt);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = h_dtype == ADAFUSE_DTYPE_F32
+                              ? launch_route(static_cast<const float*>(h), T, d, ldh, Wr, g, rt, ctx, s)
+                              : launch_route(static_cast<const __nv_bfloat16*>(h), T, d, ldh, Wr, g, rt, ctx, s);
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "route launch");
 }
 
