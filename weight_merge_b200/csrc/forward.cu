@@ -89,7 +89,7 @@ cudaError_t launch_route_as(const H* h, int64_t T, int64_t d, int64_t ldh, const
     ensure_smem_attr(kernel, smem, ctx->device);
     const int h_piece = ldh * (int64_t)sizeof(H) % 16 == 0 ? 16 : 8;
     const int w_piece = (reinterpret_cast<uintptr_t>(Wr) & 15u) == 0 ? 16 : 4;
-    return launch_clusters(kernel, groups * C, kRouteThreads, smem, C, false, s, h, T, d, ldh, Wr, g, route, C,
+    return launch_clusters(kernel, groups * C, kRouteThreads, smem, C, s, h, T, d, ldh, Wr, g, route, C,
                            h_piece, w_piece);
 }
 

@@ -92,28 +92,27 @@ inline RoutedLayout routed_layout(const adafuse_ctx* ctx, const PairDesc& pd, in
     return w;
 }
 
+// A launch on clusters that may be set up while the launch before it ends:
+// every kernel launched here executes griddepcontrol.wait before it touches
+// memory an earlier launch may write (or relies on one that did).
 template <typename Kernel, typename... Args>
-cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t smem, int cluster, bool overlap,
-                            cudaStream_t s, const Args&... args) {
+cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                            const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    int n = 0;
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = (unsigned)cluster;
-    attr[n].val.clusterDim.y = 1;
-    attr[n].val.clusterDim.z = 1;
-    ++n;
-    if (overlap) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    const unsigned n = 2;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = (unsigned)n;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -129,32 +128,32 @@ inline int skinny_split(int64_t tiles, int nsteps, int sm_count) {
 }
 
 template <int TN, int MODE>
-cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMap& map_b, bool overlap,
-                          const adafuse_ctx* ctx, cudaStream_t s) {
+cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMap& map_b, const adafuse_ctx* ctx,
+                          cudaStream_t s) {
     using C = SkinnyConfig<TN>;
     CUtensorMap map_x, map_v;
     std::memset(&map_v, 0, sizeof map_v);
     if (!encode_rows(&map_x, L.p.x, L.p.T, L.p.in, L.p.ldx, TN)) return cudaErrorInvalidValue;
     if (L.vsteps > 0 && !encode_v(&map_v, L, TN)) return cudaErrorInvalidValue;
     L.tok_tiles = (int)ceil_div(L.p.T, TN);
-    const int64_t tiles = ceil_div(L.rows, 128) * L.tok_tiles;
+    const int64_t tiles = ceil_div(L.rows, L.tile_rows) * L.tok_tiles;
     const int S = skinny_split(tiles, L.xsteps + L.vsteps, ctx->sm_count);
     if (tiles * S > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int stages = C::stages(tiles * S <= ctx->sm_count ? 1 : 2);
     auto kernel = linear_skinny_kernel<TN, MODE>;
     ensure_smem_attr(kernel, C::smem_bytes(C::stages(1)), ctx->device);
-    return launch_clusters(kernel, tiles * S, kSkinnyThreads, C::smem_bytes(stages), S, overlap, s, L, map_w,
+    return launch_clusters(kernel, tiles * S, kSkinnyThreads, C::smem_bytes(stages), S, s, L, map_w,
                            map_x, map_b, map_v, S, stages);
 }
 
 template <int MODE>
 cudaError_t launch_skinny_any(const TcLinear& L, const CUtensorMap& map_w, const CUtensorMap& map_b,
-                              bool overlap, const adafuse_ctx* ctx, cudaStream_t s) {
+                              const adafuse_ctx* ctx, cudaStream_t s) {
     const int64_t T = L.p.T;
-    if (T <= 16) return launch_skinny<16, MODE>(L, map_w, map_b, overlap, ctx, s);
-    if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, overlap, ctx, s);
-    if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, overlap, ctx, s);
-    return launch_skinny<128, MODE>(L, map_w, map_b, overlap, ctx, s);
+    if (T <= 16) return launch_skinny<16, MODE>(L, map_w, map_b, ctx, s);
+    if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, ctx, s);
+    if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, ctx, s);
+    return launch_skinny<128, MODE>(L, map_w, map_b, ctx, s);
 }
 
 // Grid of the stream kernel: two CTAs an SM less `reserve` CTAs, or, where
@@ -176,11 +175,10 @@ cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, fl
     int S = 1, reserve = 0;
     if (MODE == kRouted) reserve = std::min(stream_grid(p.E * p.r, p.in, 0, ctx->sm_count, &S), ctx->sm_count);
     const int grid = stream_grid(rows, p.in, reserve, ctx->sm_count, &S);
-    const bool overlap = MODE == kRouted;
     const bool wide = p.in % 16 == 0 && (reinterpret_cast<uintptr_t>(W) & 31u) == 0;
-    return wide ? launch_clusters(linear_stream_kernel<MODE, true>, grid, kStreamThreads, 0, S, overlap, s, p,
+    return wide ? launch_clusters(linear_stream_kernel<MODE, true>, grid, kStreamThreads, 0, S, s, p,
                                   W, rows, u, S)
-                : launch_clusters(linear_stream_kernel<MODE, false>, grid, kStreamThreads, 0, S, overlap, s, p,
+                : launch_clusters(linear_stream_kernel<MODE, false>, grid, kStreamThreads, 0, S, s, p,
                                   W, rows, u, S);
 }
 
@@ -217,7 +215,7 @@ inline bool pair_is_faster(const TcLinear& L, int sm_count) {
 }
 
 template <bool CHUNKED>
-cudaError_t launch_pair(TcLinear L, bool overlap, const adafuse_ctx* ctx, cudaStream_t s) {
+cudaError_t launch_pair(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
     L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
     const int64_t most = ctx->sm_count / 2;
     double us;
@@ -233,22 +231,22 @@ cudaError_t launch_pair(TcLinear L, bool overlap, const adafuse_ctx* ctx, cudaSt
     const int64_t tiles = L.tok_tiles * ceil_div(L.p.out, BN);
     auto kernel = linear_pair_kernel<CHUNKED>;
     ensure_smem_attr(kernel, kPairSmemBytes, ctx->device);
-    return launch_clusters(kernel, 2 * std::min(tiles, most), kPairThreads, kPairSmemBytes, 2, overlap, s, L,
+    return launch_clusters(kernel, 2 * std::min(tiles, most), kPairThreads, kPairSmemBytes, 2, s, L,
                            map_w, map_x, map_b, map_v, BN);
 }
 
 // y of one product; L carries V's geometry when the adapters are part of it.
 inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
     L.rows = L.p.out;
+    L.tile_rows = 128;
     L.xsteps = (int)ceil_div(L.p.in, 64);
-    const bool overlap = L.vsteps > 0;
     if (L.p.T > 128 && pair_is_faster(L, ctx->sm_count))
-        return L.p.f32 ? launch_pair<true>(L, overlap, ctx, s) : launch_pair<false>(L, overlap, ctx, s);
+        return L.p.f32 ? launch_pair<true>(L, ctx, s) : launch_pair<false>(L, ctx, s);
     CUtensorMap map_w, map_b;
     std::memset(&map_b, 0, sizeof map_b);
     if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
     if (L.vsteps > 0 && !encode_b(&map_b, L, 128)) return cudaErrorInvalidValue;
-    return launch_skinny_any<kProduct>(L, map_w, map_b, overlap, ctx, s);
+    return launch_skinny_any<kProduct>(L, map_w, map_b, ctx, s);
 }
 
 // V of a routed product.
@@ -256,10 +254,11 @@ inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t 
     CUtensorMap map_a, none;
     std::memset(&none, 0, sizeof none);
     L.rows = L.p.E * L.p.r;
+    L.tile_rows = 128 / L.p.r * L.p.r;
     L.xsteps = (int)ceil_div(L.p.in, 64);
     L.vsteps = 0;
     if (!encode_rows(&map_a, L.p.A, L.rows, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
-    return launch_skinny_any<kDown>(L, map_a, none, false, ctx, s);
+    return launch_skinny_any<kDown>(L, map_a, none, ctx, s);
 }
 
 }  // namespace adafuse

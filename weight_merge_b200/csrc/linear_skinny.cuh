@@ -44,6 +44,7 @@ struct TcLinear {
                        // otherwise as eight [rows][8] groups
     uint16_t* v;       // [terms][T][E * rp]
     int rows;          // kDown: E * r; otherwise out
+    int tile_rows;     // rows of a tile that are its own: 128, or whole experts of kDown
     int tok_tiles;     // token tiles
 };
 
@@ -78,6 +79,11 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return true;
 }
 
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -241,35 +247,28 @@ __device__ __forceinline__ float gate_of(const LinearParams& p, int64_t t, int e
     return p.s * g;
 }
 
-// Eight consecutive rows of the stacked A (from c, a multiple of 8) for token
-// t: V = gate * (x A^T) as bf16 terms, the first the value rounded, the second
-// what that rounding left.  A token that did not choose the expert gets exact
-// zeros, whatever its x holds.
-__device__ __forceinline__ void finish_down8(const TcLinear& L, int64_t t, int c, const float (&u)[8],
+// Eight columns of V for token t and expert e, from k (a multiple of 8): gate *
+// (x A^T) as bf16 terms, the first the value rounded, the second what that
+// rounding left; zeros past the rank.  A token that did not choose the expert
+// gets exact zeros, whatever its x holds.
+__device__ __forceinline__ void finish_down8(const TcLinear& L, int64_t t, int e, int k, const float (&u)[8],
                                              int& bad) {
     const LinearParams& p = L.p;
-    const int64_t width = (int64_t)p.E * L.rp;
-    const int64_t plane = p.T * width;
-    int last = -1;
-    float g = 0.f;
-    for (int i = 0; i < 8; ++i) {
-        if (c + i >= L.rows) break;
-        const int e = (c + i) / p.r, k = (c + i) % p.r;
-        if (e != last) {
-            g = gate_of(p, t, e, bad);
-            last = e;
-        }
-        const float val = g != 0.f ? g * u[i] : 0.f;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(val);
-        uint16_t* dst = L.v + t * width + (int64_t)e * L.rp + k;
-        dst[0] = __bfloat16_as_ushort(hi);
-        if (L.terms == 2) dst[plane] = __bfloat16_as_ushort(__float2bfloat16_rn(val - __bfloat162float(hi)));
-        if (k == p.r - 1)
-            for (int z = 1; z <= L.rp - p.r; ++z) {
-                dst[z] = 0;
-                if (L.terms == 2) dst[plane + z] = 0;
-            }
+    const float g = gate_of(p, t, e, bad);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = g != 0.f && k + 2 * i < p.r ? g * u[2 * i] : 0.f;
+        const float b = g != 0.f && k + 2 * i + 1 < p.r ? g * u[2 * i + 1] : 0.f;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+        hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+        lo[i] = *reinterpret_cast<const uint32_t*>(&l);
     }
+    const int64_t width = (int64_t)p.E * L.rp;
+    uint16_t* dst = L.v + t * width + (int64_t)e * L.rp + k;   // 16-byte aligned: rp and k are multiples of 8
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (L.terms == 2) *reinterpret_cast<uint4*>(dst + p.T * width) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 template <int TN>
@@ -280,12 +279,13 @@ struct SkinnyConfig {
     static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
     static constexpr int kAccs = TN == 128 ? 2 : TN == 64 ? 4 : 8;   // TMEM accumulators
     static constexpr uint32_t kTmemCols = kAccs * TN;                // 128 or 256: two CTAs fit
+    static constexpr uint32_t stages_min() { return 108u * 1024u / kStageBytes; }
     // stages of a launch with `ctas` (1 or 2) CTAs an SM
     static constexpr int stages(int ctas) {
         return (int)((ctas == 1 ? 216u * 1024u : 108u * 1024u) / kStageBytes);
     }
     static constexpr uint32_t smem_bytes(int stages) { return 1024 + stages * kStageBytes + 8 * (2 * stages + 1) + 16; }
-    static_assert(TN * 128 * 4 <= 3 * kStageBytes, "the partial tile reuses the ring");
+    static_assert(TN * 128 * 4 + 32 <= stages_min() * kStageBytes, "the partial tile reuses the ring");
     static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 };
 
@@ -307,10 +307,9 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    if (MODE == kDown) pdl_launch_dependents();
     const int q = (int)(blockIdx.x % (unsigned)S);
     const int64_t tile = blockIdx.x / (unsigned)S;
-    const int row0 = (int)(tile / L.tok_tiles) * 128;
+    const int row0 = (int)(tile / L.tok_tiles) * L.tile_rows;
     const int64_t tok0 = (tile % L.tok_tiles) * TN;
     const int nsteps = L.xsteps + L.vsteps;
     const int k0 = (int)((int64_t)q * nsteps / S), k1 = (int)((int64_t)(q + 1) * nsteps / S);
@@ -334,6 +333,11 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The set-up above overlaps the end of the launch before this one.  A routed
+    // product goes on: its x, W and B were complete before the kDown launch let
+    // it start, and only V is waited for.
+    if (MODE == kDown || L.vsteps == 0) pdl_wait();
+    if (MODE == kDown) pdl_launch_dependents();
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(L.p.status, ADAFUSE_STATUS_TIMEOUT);
@@ -457,8 +461,11 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     }
     // ---- this CTA's slice of the tile: sum over the cluster, epilogue, store
     const int ntok = (int)(L.p.T - tok0 < TN ? L.p.T - tok0 : TN);
-    const int nrow = L.rows - row0 < 128 ? L.rows - row0 : 128;
-    const int groups = ntok * 16;
+    const int nrow = L.rows - row0 < L.tile_rows ? L.rows - row0 : L.tile_rows;
+    // eight columns each: of y (16 groups a token), or of an expert's V
+    const int per_expert = MODE == kDown ? L.rp >> 3 : 0;
+    const int per_tok = MODE == kDown ? nrow / L.p.r * per_expert : 16;
+    const int groups = ntok * per_tok;
     const int g0 = (int)((int64_t)q * groups / S), g1 = (int)((int64_t)(q + 1) * groups / S);
     SideCols<8> side;
     // what does not depend on the sums is requested before they are complete
@@ -474,7 +481,13 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
         int bad = 0;
 #pragma unroll 1
         for (int gi = g0 + (int)threadIdx.x; gi < g1; gi += kSkinnyThreads) {
-            const int tok = gi >> 4, r8 = (gi & 15) * 8;
+            const int tok = MODE == kDown ? gi / per_tok : gi >> 4, in_tok = gi - tok * per_tok;
+            int r8 = in_tok * 8, e = 0, k = 0;
+            if constexpr (MODE == kDown) {
+                e = in_tok / per_expert;
+                k = (in_tok - e * per_expert) * 8;
+                r8 = e * L.p.r + k;
+            }
             if (r8 < nrow) {
                 float v[8];
 #pragma unroll
@@ -484,12 +497,19 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
                 for (int c = 0; c < S; ++c) {
                     uint32_t a = off;
                     if (S > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(off), "r"(c));
-                    const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
-                    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-                    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                    if (MODE == kDown && (L.p.r & 7) != 0) {
+                        // an expert's rows start anywhere; reads past the tile's
+                        // last row stay inside the ring and are left out later
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] += ld_cluster_f1(a + 4u * i);
+                    } else {
+                        const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
+                        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+                        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                    }
                 }
                 if constexpr (MODE == kDown)
-                    finish_down8(L, tok0 + tok, row0 + r8, v, bad);
+                    finish_down8(L, tok0 + tok, row0 / L.p.r + e, k, v, bad);
                 else
                     finish_cols(L.p, tok0 + tok, row0 + r8, v, side);
             }

@@ -26,10 +26,8 @@ namespace adafuse {
 
 enum : int { kProduct = 0, kDown = 1, kRouted = 2 };
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+using sm100::pdl_launch_dependents;
+using sm100::pdl_wait;
 
 constexpr int kStreamWarps = 16;
 constexpr int kStreamThreads = 32 * kStreamWarps;
@@ -133,6 +131,9 @@ linear_stream_kernel(const LinearParams p, const uint16_t* __restrict__ W, const
     const int height = units > 0 ? (row_end - row_begin + units - 1) / units : kStreamRows;
     const int T = (int)p.T;
 
+    // A routed product starts while the kDown launch before it runs: its x and W
+    // were complete before that launch let it start, and u is waited for below.
+    if constexpr (MODE != kRouted) pdl_wait();
     if constexpr (MODE == kDown) {
         pdl_launch_dependents();
         // experts that some token chose; a unit of rows none of them owns is

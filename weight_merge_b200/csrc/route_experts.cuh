@@ -493,6 +493,7 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     ww[0] = 0.f;
     if (EMAX > 32) ww[EMAX > 32 ? 1 : 0] = 0.f;
 
+    sm100::pdl_wait();   // set-up overlaps the end of the launch before this one
 #pragma unroll
     for (int s = 0; s < kRouteStages - 1; ++s) load_chunk(q + (int64_t)s * C, s);
     int stage = 0;

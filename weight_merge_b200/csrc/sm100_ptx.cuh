@@ -30,6 +30,13 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
+// Programmatic dependent launch: wait until the launches this one depends on are
+// complete and their writes visible; let the next launch start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- mbarrier --------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
