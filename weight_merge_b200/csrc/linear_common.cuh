@@ -163,6 +163,109 @@ __device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, in
     }
 }
 
+// A warp's 32 tokens x 16 columns of y from the finished products.  v: lane =
+// token.  Stored from there, a warp's 16-byte pieces would fall into 32 rows and
+// half of each 32-byte sector (a 256 x 240 fp32 tile took 10 us longer); so the
+// block turns through `turn`, 2 KB of the warp's own shared memory whose 16-byte
+// pieces are permuted against bank conflicts, and leaves in pieces that lie next
+// to each other: F32: 4 lanes a token, 4 columns each, 4 times 8 tokens;
+// otherwise 2 lanes, 8 columns, twice 16 tokens.
+template <bool F32>
+struct BlockSide {
+    static constexpr int kIters = F32 ? 4 : 2, kCols = F32 ? 4 : 8;
+    float mul[kIters][kCols], res[kIters][kCols];
+};
+
+__device__ __forceinline__ void load_cols(const void* base, int64_t at, float (&w)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+}
+__device__ __forceinline__ void load_cols(const void* base, int64_t at, float (&w)[8]) {
+    load8(base, at, 0, w);
+}
+
+// Requests the factor and the residual of the block at token tok0, column col0.
+template <bool F32>
+__device__ __forceinline__ void load_block(const LinearParams& p, int64_t tok0, int col0, int lane,
+                                           BlockSide<F32>& side) {
+    using S = BlockSide<F32>;
+    constexpr int kLanes = 16 / S::kCols;
+    const int col = col0 + lane % kLanes * S::kCols;
+#pragma unroll
+    for (int j = 0; j < S::kIters; ++j) {
+        const int64_t t = tok0 + lane / kLanes + j * (32 / kLanes);
+        if (t < p.T && col < p.out) {
+            if (p.mul != nullptr) load_cols(p.mul, t * p.ldmul + col, side.mul[j]);
+            if (p.res != nullptr) load_cols(p.res, t * p.ldres + col, side.res[j]);
+        }
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void finish_block(const LinearParams& p, int64_t tok0, int col0, int lane,
+                                             const float (&v)[16], const BlockSide<F32>& side, uint8_t* turn) {
+    using S = BlockSide<F32>;
+    constexpr int kLanes = 16 / S::kCols;
+    auto piece = [&](int row, int c) {   // the 16-byte piece of columns 4c .. 4c + 3
+        return turn + row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<float4*>(piece(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+    const int col = col0 + lane % kLanes * S::kCols;
+    float bias[S::kCols];
+    if (p.bias != nullptr && col < p.out) {
+#pragma unroll
+        for (int i = 0; i < S::kCols; ++i) bias[i] = __ldg(p.bias + col + i);
+    }
+    float w[S::kIters * S::kCols];
+#pragma unroll
+    for (int j = 0; j < S::kIters; ++j)
+#pragma unroll
+        for (int c = 0; c < S::kCols / 4; ++c) {
+            const float4 f = *reinterpret_cast<const float4*>(
+                piece(lane / kLanes + j * (32 / kLanes), lane % kLanes * (S::kCols / 4) + c));
+            w[j * S::kCols + 4 * c] = f.x;
+            w[j * S::kCols + 4 * c + 1] = f.y;
+            w[j * S::kCols + 4 * c + 2] = f.z;
+            w[j * S::kCols + 4 * c + 3] = f.w;
+        }
+    __syncwarp();
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < S::kIters * S::kCols; ++i) w[i] += bias[i % S::kCols];
+    }
+    apply_act(w, p.act);
+#pragma unroll
+    for (int j = 0; j < S::kIters; ++j) {
+        const int64_t t = tok0 + lane / kLanes + j * (32 / kLanes);
+        if (t >= p.T || col >= p.out) continue;
+        float* o = &w[j * S::kCols];
+        if (p.mul != nullptr) {
+#pragma unroll
+            for (int i = 0; i < S::kCols; ++i) o[i] *= side.mul[j][i];
+        }
+        if (p.res != nullptr) {
+#pragma unroll
+            for (int i = 0; i < S::kCols; ++i) o[i] += side.res[j][i];
+        }
+        if constexpr (F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + t * p.ldy + col) =
+                make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + t * p.ldy + col) =
+                make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    }
+}
+
 // Slot j of token t's record: false for an empty or bad slot; a bad one sets
 // its bits in *bad.
 __device__ __forceinline__ bool route_slot(const int32_t* routes, int slots, int E, int64_t t, int j,

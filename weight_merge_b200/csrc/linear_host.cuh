@@ -182,21 +182,20 @@ cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, fl
                                   W, rows, u, S);
 }
 
-// Estimated time (us) of a 64-column step of a 256 x BN tile on a CTA pair
-// (measured 0.18 at BN = 128 to 0.34 at 256 with every SM busy).
-inline double pair_step_us(int bn) { return 0.02 + 0.00125 * bn; }
-
 // Tile width of the pair kernel: the multiple of 16 in [128, 256] with the least
 // estimated time for the longest pair's share, the narrower among equals (their
-// tiles finish sooner).  *us: that estimate for nsteps.
+// tiles finish sooner).  A 64-column step of a tile takes about (BN + 64) ns
+// (T = 512 4096 -> 4096, one round: 18.4, 21.1, 25.6, 26.8 us at BN = 128, 192,
+// 240, 256; T = 4096, 7, 5, 4 and 4 rounds: 109.7, 100.6, 93.7, 94.9 us).  *us:
+// the estimate for nsteps.
 inline int pair_width(int64_t tok_tiles, int out, int64_t pairs, int nsteps, double* us) {
     int best = kPairMaxCols;
-    double least = 1e300;
+    int64_t least = INT64_MAX;
     for (int bn = kPairMaxCols; bn >= 128; bn -= 16) {
-        const double t = (double)ceil_div(tok_tiles * ceil_div(out, bn), pairs) * pair_step_us(bn);
-        if (t <= least) { least = t; best = bn; }
+        const int64_t ns = ceil_div(tok_tiles * ceil_div(out, bn), pairs) * (bn + 64);
+        if (ns <= least) { least = ns; best = bn; }
     }
-    *us = 6.0 + least * nsteps;
+    *us = 6.0 + 1e-3 * (double)least * nsteps;
     return best;
 }
 
@@ -214,7 +213,7 @@ inline bool pair_is_faster(const TcLinear& L, int sm_count) {
     return pair_us <= skinny_us;
 }
 
-template <bool CHUNKED>
+template <bool F32>
 cudaError_t launch_pair(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
     L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
     const int64_t most = ctx->sm_count / 2;
@@ -229,7 +228,7 @@ cudaError_t launch_pair(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
     if (L.vsteps > 0 && (!encode_b(&map_b, L, BN / 2) || !encode_v(&map_v, L, 128)))
         return cudaErrorInvalidValue;
     const int64_t tiles = L.tok_tiles * ceil_div(L.p.out, BN);
-    auto kernel = linear_pair_kernel<CHUNKED>;
+    auto kernel = linear_pair_kernel<F32>;
     ensure_smem_attr(kernel, kPairSmemBytes, ctx->device);
     return launch_clusters(kernel, 2 * std::min(tiles, most), kPairThreads, kPairSmemBytes, 2, s, L,
                            map_w, map_x, map_b, map_v, BN);

@@ -11,7 +11,7 @@
 // comes from memory once and x stays in L2.  BN is a launch parameter (a
 // multiple of 16): the host takes the width whose tiles fill whole rounds.
 //
-// CHUNKED (fp32 outputs): tensor-core accumulators drop low bits on every
+// F32 (fp32 outputs): tensor-core accumulators drop low bits on every
 // 16-deep step (measured: 4e-6 of the result after 4096 products, 1.2e-5 after
 // 11008), so the contraction is cut into chunks of kChunkSteps steps, each
 // started from zero, and the epilogue adds them in registers in fp32.  A bf16
@@ -38,10 +38,12 @@ constexpr int kChunkSteps = 16;
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairXBytes = 128 * 128;
 constexpr uint32_t kPairStageBytes = 2 * kPairXBytes;   // x, then up to 128 rows of W
-constexpr uint32_t kPairSmemBytes = 1024 + kPairStages * kPairStageBytes + 8 * (2 * kPairStages + 4) + 16;
+constexpr uint32_t kTurnBytes = 32 * 16 * 4;              // per epilogue warp, see finish_block
+constexpr uint32_t kPairSmemBytes =
+    1024 + kPairStages * kPairStageBytes + kPairEpiWarps * kTurnBytes + 8 * (2 * kPairStages + 4) + 16;
 static_assert(kPairSmemBytes <= 232448, "shared memory");
 
-template <bool CHUNKED>
+template <bool F32>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ CUtensorMap map_w,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_b,
@@ -51,7 +53,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     // the same offsets in both CTAs: MMA descriptors name one address for both
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStageBytes);   // even CTA's used
+    uint8_t* turns = ring + kPairStages * kPairStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(turns + kPairEpiWarps * kTurnBytes);   // even CTA's used
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;    // [2]
     uint64_t* acc_empty = acc_full + 2;         // [2], even CTA's used
@@ -138,8 +141,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
             };
             for (int64_t t = t_first; ok && t < tiles; t += t_stride) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < nsteps; c0 += CHUNKED ? kChunkSteps : nsteps) {
-                    const int c1 = CHUNKED && c0 + kChunkSteps < nsteps ? c0 + kChunkSteps : nsteps;
+                for (int c0 = 0; c0 < nsteps; c0 += F32 ? kChunkSteps : nsteps) {
+                    const int c1 = F32 && c0 + kChunkSteps < nsteps ? c0 + kChunkSteps : nsteps;
                     ok = wait_phase(smem_u32(&acc_empty[buf]), aph ^ 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -183,17 +186,17 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
         }
     } else if (warp >= 4) {
         const int group = (warp - 4) >> 2;
+        uint8_t* turn = turns + (warp - 4) * kTurnBytes;
         const int blocks = BN / 16;                       // 16-column blocks: group, group + 4, ...
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
-        const int chunks = CHUNKED ? (nsteps + kChunkSteps - 1) / kChunkSteps : 1;
+        const int chunks = F32 ? (nsteps + kChunkSteps - 1) / kChunkSteps : 1;
         int buf = 0;
         uint32_t aph = 0;
         bool ok = true;
         for (int64_t t = t_first; ok && t < tiles; t += t_stride) {
-            const int64_t tok = (t % L.tok_tiles) * kPairTokens + q * 128 + (warp & 3) * 32 + lane;
+            const int64_t tok0 = (t % L.tok_tiles) * kPairTokens + q * 128 + (warp & 3) * 32;
             const int col0 = (int)(t / L.tok_tiles) * BN;
-            const bool mine = tok < L.p.T;
             auto await_chunk = [&]() {
                 ok = wait_phase(smem_u32(&acc_full[buf]), aph, abort_flag, 4 * kWaitClocks);
                 tc_fence_after();
@@ -207,7 +210,7 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
                 if (buf == 0) aph ^= 1;
             };
             uint32_t src;
-            if constexpr (CHUNKED) {
+            if constexpr (F32) {
                 // the chunks' sums in registers; with the last one they go back
                 // to TMEM, from where one short loop takes them
                 float acc[4][16];
@@ -248,11 +251,11 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
 #pragma unroll 1
             for (int cb = group; cb < blocks; cb += 4) {
                 float v[16];
-                SideCols<16> side;
-                if (mine) side.load(L.p, tok, col0 + 16 * cb);
+                BlockSide<F32> side;
+                load_block<F32>(L.p, tok0, col0 + 16 * cb, lane, side);
                 tmem_ld16(src + 16u * cb, v);
                 tmem_wait_ld();
-                if (mine) finish_cols(L.p, tok, col0 + 16 * cb, v, side);
+                finish_block<F32>(L.p, tok0, col0 + 16 * cb, lane, v, side, turn);
             }
             release_chunk();
         }
