@@ -173,7 +173,9 @@ __device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, in
 template <bool F32>
 struct BlockSide {
     static constexpr int kIters = F32 ? 4 : 2, kCols = F32 ? 4 : 8;
-    float mul[kIters][kCols], res[kIters][kCols];
+    // the factor ahead of its use for bf16 only: in fp32, the rarer case, its
+    // registers would spill
+    float mul[F32 ? 1 : kIters][kCols], res[kIters][kCols];
 };
 
 __device__ __forceinline__ void load_cols(const void* base, int64_t at, float (&w)[4]) {
@@ -195,7 +197,7 @@ __device__ __forceinline__ void load_block(const LinearParams& p, int64_t tok0, 
     for (int j = 0; j < S::kIters; ++j) {
         const int64_t t = tok0 + lane / kLanes + j * (32 / kLanes);
         if (t < p.T && col < p.out) {
-            if (p.mul != nullptr) load_cols(p.mul, t * p.ldmul + col, side.mul[j]);
+            if (!F32 && p.mul != nullptr) load_cols(p.mul, t * p.ldmul + col, side.mul[F32 ? 0 : j]);
             if (p.res != nullptr) load_cols(p.res, t * p.ldres + col, side.res[j]);
         }
     }
@@ -243,8 +245,10 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, int64_t tok0
         if (t >= p.T || col >= p.out) continue;
         float* o = &w[j * S::kCols];
         if (p.mul != nullptr) {
+            float m[S::kCols];
+            if constexpr (F32) load_cols(p.mul, t * p.ldmul + col, m);
 #pragma unroll
-            for (int i = 0; i < S::kCols; ++i) o[i] *= side.mul[j][i];
+            for (int i = 0; i < S::kCols; ++i) o[i] *= F32 ? m[i] : side.mul[F32 ? 0 : j][i];
         }
         if (p.res != nullptr) {
 #pragma unroll

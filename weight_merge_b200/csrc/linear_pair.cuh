@@ -13,9 +13,10 @@
 //
 // F32 (fp32 outputs): tensor-core accumulators drop low bits on every
 // 16-deep step (measured: 4e-6 of the result after 4096 products, 1.2e-5 after
-// 11008), so the contraction is cut into chunks of kChunkSteps steps, each
-// started from zero, and the epilogue adds them in registers in fp32.  A bf16
-// output does not see the difference and takes one chunk.
+// 11008), so the contraction is cut into chunks of at most kChunkSteps steps,
+// each started from zero, and the epilogue adds them in registers in fp32 (about
+// 0.5 us a chunk of the tensor cores' time; 1.4e-6 of the result is left).  A
+// bf16 output does not see the difference and takes one chunk.
 //
 // Routed products: after x and W come V and the stacked B, as in
 // linear_skinny.cuh.
@@ -34,7 +35,7 @@ constexpr int kPairThreads = 640;
 constexpr int kPairEpiWarps = 16;
 constexpr int kPairTokens = 256;
 constexpr int kPairMaxCols = 256;
-constexpr int kChunkSteps = 16;
+constexpr int kChunkSteps = 24;
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairXBytes = 128 * 128;
 constexpr uint32_t kPairStageBytes = 2 * kPairXBytes;   // x, then up to 128 rows of W
@@ -94,6 +95,9 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     };
 
     const int nsteps = L.xsteps + L.vsteps;
+    // even chunks of at most kChunkSteps
+    const int chunks = F32 ? (nsteps + kChunkSteps - 1) / kChunkSteps : 1;
+    const int chunk_steps = (nsteps + chunks - 1) / chunks;
     const int col_tiles = (L.p.out + BN - 1) / BN;
     const int64_t tiles = (int64_t)L.tok_tiles * col_tiles;
     const int64_t t_first = cluster_id_x(), t_stride = cluster_count_x();
@@ -141,8 +145,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
             };
             for (int64_t t = t_first; ok && t < tiles; t += t_stride) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < nsteps; c0 += F32 ? kChunkSteps : nsteps) {
-                    const int c1 = F32 && c0 + kChunkSteps < nsteps ? c0 + kChunkSteps : nsteps;
+                for (int c0 = 0; c0 < nsteps; c0 += chunk_steps) {
+                    const int c1 = c0 + chunk_steps < nsteps ? c0 + chunk_steps : nsteps;
                     ok = wait_phase(smem_u32(&acc_empty[buf]), aph ^ 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -190,7 +194,6 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
         const int blocks = BN / 16;                       // 16-column blocks: group, group + 4, ...
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
-        const int chunks = F32 ? (nsteps + kChunkSteps - 1) / kChunkSteps : 1;
         int buf = 0;
         uint32_t aph = 0;
         bool ok = true;
@@ -209,39 +212,41 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
                 buf ^= 1;
                 if (buf == 0) aph ^= 1;
             };
-            uint32_t src;
+            uint32_t src = 0;
             if constexpr (F32) {
-                // the chunks' sums in registers; with the last one they go back
-                // to TMEM, from where one short loop takes them
+                // The chunks' sums in registers; with the last chunk they go
+                // back to TMEM, from where the loop below takes them.  (Held in
+                // registers through that loop they would spill, and with the
+                // ring in shared memory L1 is too small for spills.)
                 float acc[4][16];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
-                auto add_chunk = [&](bool back) {
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    src = await_chunk();
+                    if (!ok || chunks == 1) break;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int cb = group + 4 * j;
                         if (cb < blocks) {
-                            float v[16];
-                            tmem_ld16(src + 16u * cb, v);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[j][i] += v[i];
-                            if (back) tmem_st16(src + 16u * cb, acc[j]);
+                            for (int h = 0; h < 16; h += 8) {
+                                float v[8];
+                                tmem_ld8(src + 16u * cb + h, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) acc[j][h + i] += v[i];
+                            }
                         }
                     }
-                };
-#pragma unroll 1
-                for (int c = 1; c < chunks; ++c) {
-                    src = await_chunk();
-                    if (!ok) break;
-                    add_chunk(false);
-                    release_chunk();
+                    if (c < chunks - 1) release_chunk();
                 }
-                if (ok) src = await_chunk();
                 if (ok && chunks > 1) {
-                    add_chunk(true);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (group + 4 * j < blocks) tmem_st16(src + 16u * (group + 4 * j), acc[j]);
                     tmem_wait_st();
                 }
             } else {
