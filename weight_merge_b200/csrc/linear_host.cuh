@@ -188,11 +188,11 @@ cudaError_t launch_stream(const LinearParams& p, const uint16_t* W, int rows, fl
 // (T = 512 4096 -> 4096, one round: 18.4, 21.1, 25.6, 26.8 us at BN = 128, 192,
 // 240, 256; T = 4096, 7, 5, 4 and 4 rounds: 109.7, 100.6, 93.7, 94.9 us).  *us:
 // the estimate for nsteps.
-inline int pair_width(int64_t tok_tiles, int out, int64_t pairs, int nsteps, double* us) {
+inline int pair_width(int64_t tok_tiles, int rows, int64_t pairs, int nsteps, double* us) {
     int best = kPairMaxCols;
     int64_t least = INT64_MAX;
     for (int bn = kPairMaxCols; bn >= 128; bn -= 16) {
-        const int64_t ns = ceil_div(tok_tiles * ceil_div(out, bn), pairs) * (bn + 64);
+        const int64_t ns = ceil_div(tok_tiles * ceil_div(rows, bn), pairs) * (bn + 64);
         if (ns <= least) { least = ns; best = bn; }
     }
     *us = 6.0 + 1e-3 * (double)least * nsteps;
@@ -206,29 +206,30 @@ inline int pair_width(int64_t tok_tiles, int out, int64_t pairs, int nsteps, dou
 inline bool pair_is_faster(const TcLinear& L, int sm_count) {
     const int nsteps = L.xsteps + L.vsteps;
     double pair_us;
-    pair_width(ceil_div(L.p.T, kPairTokens), L.p.out, sm_count / 2, nsteps, &pair_us);
-    const int64_t tiles = ceil_div(L.p.out, 128) * ceil_div(L.p.T, 128);
+    pair_width(ceil_div(L.p.T, kPairTokens), L.rows, sm_count / 2, nsteps, &pair_us);
+    const int64_t tiles = ceil_div(L.rows, L.tile_rows) * ceil_div(L.p.T, 128);
     const int S = skinny_split(tiles, nsteps, sm_count);
     const double skinny_us = 7.0 + (double)(ceil_div(tiles * S, sm_count) * ceil_div(nsteps, S)) * 0.19;
     return pair_us <= skinny_us;
 }
 
-template <bool F32>
-cudaError_t launch_pair(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
+// W: the [L.rows, in] operand, the weight or (kDown) the stacked A.
+template <bool F32, int MODE>
+cudaError_t launch_pair(TcLinear L, const uint16_t* W, const adafuse_ctx* ctx, cudaStream_t s) {
     L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
     const int64_t most = ctx->sm_count / 2;
     double us;
-    const int BN = pair_width(L.tok_tiles, L.p.out, most, L.xsteps + L.vsteps, &us);
+    const int BN = pair_width(L.tok_tiles, L.rows, most, L.xsteps + L.vsteps, &us);
     CUtensorMap map_w, map_x, map_b, map_v;
     std::memset(&map_b, 0, sizeof map_b);
     std::memset(&map_v, 0, sizeof map_v);
-    if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, BN / 2) ||
+    if (!encode_rows(&map_w, W, L.rows, L.p.in, L.p.in, BN / 2) ||
         !encode_rows(&map_x, L.p.x, L.p.T, L.p.in, L.p.ldx, 128))
         return cudaErrorInvalidValue;
     if (L.vsteps > 0 && (!encode_b(&map_b, L, BN / 2) || !encode_v(&map_v, L, 128)))
         return cudaErrorInvalidValue;
-    const int64_t tiles = L.tok_tiles * ceil_div(L.p.out, BN);
-    auto kernel = linear_pair_kernel<F32>;
+    const int64_t tiles = L.tok_tiles * ceil_div(L.rows, BN);
+    auto kernel = linear_pair_kernel<F32, MODE>;
     ensure_smem_attr(kernel, kPairSmemBytes, ctx->device);
     return launch_clusters(kernel, 2 * std::min(tiles, most), kPairThreads, kPairSmemBytes, 2, s, L,
                            map_w, map_x, map_b, map_v, BN);
@@ -240,7 +241,7 @@ inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream
     L.tile_rows = 128;
     L.xsteps = (int)ceil_div(L.p.in, 64);
     if (L.p.T > 128 && pair_is_faster(L, ctx->sm_count))
-        return L.p.f32 ? launch_pair<true>(L, ctx, s) : launch_pair<false>(L, ctx, s);
+        return L.p.f32 ? launch_pair<true, kProduct>(L, L.p.W, ctx, s) : launch_pair<false, kProduct>(L, L.p.W, ctx, s);
     CUtensorMap map_w, map_b;
     std::memset(&map_b, 0, sizeof map_b);
     if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
@@ -256,6 +257,9 @@ inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t 
     L.tile_rows = 128 / L.p.r * L.p.r;
     L.xsteps = (int)ceil_div(L.p.in, 64);
     L.vsteps = 0;
+    if (L.p.T > 128 && L.rp == L.p.r && pair_is_faster(L, ctx->sm_count))
+        return L.terms == 2 ? launch_pair<true, kDown>(L, L.p.A, ctx, s)
+                            : launch_pair<false, kDown>(L, L.p.A, ctx, s);
     if (!encode_rows(&map_a, L.p.A, L.rows, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
     return launch_skinny_any<kDown>(L, map_a, none, ctx, s);
 }

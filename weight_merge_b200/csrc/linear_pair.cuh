@@ -11,7 +11,7 @@
 // comes from memory once and x stays in L2.  BN is a launch parameter (a
 // multiple of 16): the host takes the width whose tiles fill whole rounds.
 //
-// F32 (fp32 outputs): tensor-core accumulators drop low bits on every
+// F32 (fp32 outputs, V of two terms): tensor-core accumulators drop low bits on every
 // 16-deep step (measured: 4e-6 of the result after 4096 products, 1.2e-5 after
 // 11008), so the contraction is cut into chunks of at most kChunkSteps steps,
 // each started from zero, and the epilogue adds them in registers in fp32 (about
@@ -19,7 +19,7 @@
 // bf16 output does not see the difference and takes one chunk.
 //
 // Routed products: after x and W come V and the stacked B, as in
-// linear_skinny.cuh.
+// linear_skinny.cuh; kDown writes V (F32: as two terms).
 //
 // Warps: 0 and 2 loads, 1 MMA (even CTA) and TMEM, 4..19 epilogue (token = 32 *
 // (warp % 4) + lane, every fourth 16-column block each four warps).
@@ -44,7 +44,30 @@ constexpr uint32_t kPairSmemBytes =
     1024 + kPairStages * kPairStageBytes + kPairEpiWarps * kTurnBytes + 8 * (2 * kPairStages + 4) + 16;
 static_assert(kPairSmemBytes <= 232448, "shared memory");
 
-template <bool F32>
+// kDown: a warp's 32 tokens x 16 columns of V (ranks that are multiples of 8, so
+// V's columns are the stacked A's rows) from the finished x A^T, turned as in
+// finish_block: 2 lanes a token, 8 columns, twice 16 tokens.
+__device__ __forceinline__ void finish_down_block(const TcLinear& L, int64_t tok0, int col0, int lane,
+                                                  const float (&v)[16], uint8_t* turn, int& bad) {
+    auto piece = [&](int row, int c) { return turn + row * 64 + ((c ^ (row >> 1 & 3)) << 4); };
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<float4*>(piece(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+    const int col = col0 + (lane & 1) * 8;
+    const int e = col / L.p.r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int row = (lane >> 1) + 16 * j;
+        const float4 a = *reinterpret_cast<const float4*>(piece(row, (lane & 1) * 2));
+        const float4 b = *reinterpret_cast<const float4*>(piece(row, (lane & 1) * 2 + 1));
+        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (tok0 + row < L.p.T && col < L.rows) finish_down8(L, tok0 + row, e, col - e * L.p.r, u, bad);
+    }
+    __syncwarp();
+}
+
+template <bool F32, int MODE>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ CUtensorMap map_w,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_b,
@@ -84,7 +107,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (L.vsteps == 0) pdl_wait();   // as in the skinny kernel
+    if (MODE == kDown || L.vsteps == 0) pdl_wait();   // as in the skinny kernel
+    if (MODE == kDown) pdl_launch_dependents();
     const uint32_t peer_abort = cluster_addr((const void*)abort_flag, q ^ 1u);
     auto fail = [&]() {
         if (!*abort_flag) {
@@ -98,7 +122,7 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     // even chunks of at most kChunkSteps
     const int chunks = F32 ? (nsteps + kChunkSteps - 1) / kChunkSteps : 1;
     const int chunk_steps = (nsteps + chunks - 1) / chunks;
-    const int col_tiles = (L.p.out + BN - 1) / BN;
+    const int col_tiles = (L.rows + BN - 1) / BN;
     const int64_t tiles = (int64_t)L.tok_tiles * col_tiles;
     const int64_t t_first = cluster_id_x(), t_stride = cluster_count_x();
 
@@ -194,7 +218,7 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
         const int blocks = BN / 16;                       // 16-column blocks: group, group + 4, ...
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
-        int buf = 0;
+        int buf = 0, bad = 0;
         uint32_t aph = 0;
         bool ok = true;
         for (int64_t t = t_first; ok && t < tiles; t += t_stride) {
@@ -256,14 +280,21 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
 #pragma unroll 1
             for (int cb = group; cb < blocks; cb += 4) {
                 float v[16];
-                BlockSide<F32> side;
-                load_block<F32>(L.p, tok0, col0 + 16 * cb, lane, side);
-                tmem_ld16(src + 16u * cb, v);
-                tmem_wait_ld();
-                finish_block<F32>(L.p, tok0, col0 + 16 * cb, lane, v, side, turn);
+                if constexpr (MODE == kDown) {
+                    tmem_ld16(src + 16u * cb, v);
+                    tmem_wait_ld();
+                    finish_down_block(L, tok0, col0 + 16 * cb, lane, v, turn, bad);
+                } else {
+                    BlockSide<F32> side;
+                    load_block<F32>(L.p, tok0, col0 + 16 * cb, lane, side);
+                    tmem_ld16(src + 16u * cb, v);
+                    tmem_wait_ld();
+                    finish_block<F32>(L.p, tok0, col0 + 16 * cb, lane, v, side, turn);
+                }
             }
             release_chunk();
         }
+        if (MODE == kDown && bad != 0) atomicOr(L.p.status, bad);
     }
 
     // teardown: after an abort copies and MMAs in flight get time to land;
