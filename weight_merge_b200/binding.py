@@ -424,6 +424,7 @@ class Switcher:
         self._types = {torch.bfloat16: ADAFUSE_DTYPE_BF16, torch.float32: ADAFUSE_DTYPE_F32}
         self.desc = make_desc(n_layers, n_targets, n_experts, rank, alpha, ts)
         self.n_layers = n_layers
+        self._lib = lib()   # the per-token calls go straight to it
         self.ctx = adafuse_create(self.desc, device)
 
     @staticmethod
@@ -508,7 +509,10 @@ class Switcher:
         rp, ldr = _rows(routes, self._i32, T, 2 * slots, "routes")
         if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of h")
-        adafuse_route_experts(self.ctx, hp, h_dtype, T, d, ldh, wp, gating, slots, rp, stream)
+        code = self._lib.adafuse_route_experts(self.ctx, hp, h_dtype, T, d, ldh, wp,
+                                               ctypes.byref(gating), slots, rp, stream or None)
+        if code:
+            raise AdafuseError(code, "adafuse_route_experts")
 
     def _linear_args(self, layer, target, x, y, bias, activation, mul, residual, base):
         if not (0 <= layer < self.n_layers and 0 <= target < self.desc.n_targets):
@@ -537,7 +541,9 @@ class Switcher:
         """y = residual + mul * act(x W^T + bias) with W of (layer, target), or
         its registered pristine copy when ``base``."""
         a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
-        adafuse_linear(self.ctx, a, stream)
+        code = self._lib.adafuse_linear(self.ctx, ctypes.byref(a), stream or None)
+        if code:
+            raise AdafuseError(code, "adafuse_linear")
 
     def linear_workspace(self, layer: int, target: int, T: int, f32: bool = False) -> int:
         """Workspace bytes of linear_routed for T tokens (``f32``: y is fp32)."""
@@ -557,7 +563,10 @@ class Switcher:
             raise ValueError("routes: one contiguous record per row of x")
         if not workspace.is_cuda:
             raise ValueError("workspace: not on a CUDA device")
-        adafuse_linear_routed(self.ctx, a, rp, slots, workspace.data_ptr(), workspace.nbytes, stream)
+        code = self._lib.adafuse_linear_routed(self.ctx, ctypes.byref(a), rp, slots,
+                                               workspace.data_ptr(), workspace.nbytes, stream or None)
+        if code:
+            raise AdafuseError(code, "adafuse_linear_routed")
 
     def set_kernel(self, kernel: int) -> None:
         adafuse_set_switch_kernel(self.ctx, kernel)

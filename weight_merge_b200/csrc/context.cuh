@@ -52,13 +52,18 @@ int cuda_fail(cudaError_t e, const char* what);
 // Restores the caller's current device on scope exit.
 struct DeviceGuard {
     int prev = -1;
-    bool ok = false;
+    bool ok = false, moved = false;
     explicit DeviceGuard(int dev) {
         if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
+        if (prev == dev) {
+            ok = true;
+        } else {
+            ok = cudaSetDevice(dev) == cudaSuccess;
+            moved = prev >= 0;
+        }
     }
     ~DeviceGuard() {
-        if (prev >= 0) cudaSetDevice(prev);
+        if (moved) cudaSetDevice(prev);
     }
 };
 

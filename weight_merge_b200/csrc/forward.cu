@@ -76,7 +76,7 @@ int linear_params(const adafuse_ctx* ctx, const adafuse_linear_args* a, LinearPa
 
 // One launch of the router: 32 tokens a CTA, their columns shared by a cluster
 // of up to 8 CTAs while that keeps the grid resident at once.
-template <int EMAX, bool VEC, typename H>
+template <int EMAX, typename H>
 cudaError_t launch_route_as(const H* h, int64_t T, int64_t d, int64_t ldh, const float* Wr, const GateParams& g,
                             int32_t* route, const adafuse_ctx* ctx, cudaStream_t s) {
     const int64_t groups = ceil_div(T, kRouteTokens), chunks = ceil_div(d, kRouteDepth);
@@ -85,7 +85,7 @@ cudaError_t launch_route_as(const H* h, int64_t T, int64_t d, int64_t ldh, const
     while (C < 8 && groups * C * 2 <= most && chunks >= C * 2) C *= 2;
     if (groups * C > INT32_MAX) return cudaErrorInvalidConfiguration;
     const size_t smem = std::max<size_t>(kRouteStages * route_stage_bytes<H>(g.E), route_tail_bytes<EMAX>());
-    auto kernel = route_experts_kernel<EMAX, VEC, H>;
+    auto kernel = route_experts_kernel<EMAX, H>;
     ensure_smem_attr(kernel, smem, ctx->device);
     const int h_piece = ldh * (int64_t)sizeof(H) % 16 == 0 ? 16 : 8;
     const int w_piece = (reinterpret_cast<uintptr_t>(Wr) & 15u) == 0 ? 16 : 4;
@@ -97,17 +97,10 @@ template <typename H>
 cudaError_t launch_route(const H* h, int64_t T, int64_t d, int64_t ldh, const float* Wr, const GateParams& g,
                          int32_t* route, const adafuse_ctx* ctx, cudaStream_t s) {
     const int E = g.E;
-    if (E <= 8)
-        return E % 2 == 0 ? launch_route_as<8, true>(h, T, d, ldh, Wr, g, route, ctx, s)
-                          : launch_route_as<8, false>(h, T, d, ldh, Wr, g, route, ctx, s);
-    if (E <= 16)
-        return E % 4 == 0 ? launch_route_as<16, true>(h, T, d, ldh, Wr, g, route, ctx, s)
-                          : launch_route_as<16, false>(h, T, d, ldh, Wr, g, route, ctx, s);
-    if (E <= 32)
-        return E % 4 == 0 ? launch_route_as<32, true>(h, T, d, ldh, Wr, g, route, ctx, s)
-                          : launch_route_as<32, false>(h, T, d, ldh, Wr, g, route, ctx, s);
-    return E % 4 == 0 ? launch_route_as<64, true>(h, T, d, ldh, Wr, g, route, ctx, s)
-                      : launch_route_as<64, false>(h, T, d, ldh, Wr, g, route, ctx, s);
+    if (E <= 8) return launch_route_as<8>(h, T, d, ldh, Wr, g, route, ctx, s);
+    if (E <= 16) return launch_route_as<16>(h, T, d, ldh, Wr, g, route, ctx, s);
+    if (E <= 32) return launch_route_as<32>(h, T, d, ldh, Wr, g, route, ctx, s);
+    return launch_route_as<64>(h, T, d, ldh, Wr, g, route, ctx, s);
 }
 
 }  // namespace
@@ -119,7 +112,7 @@ int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int6
                           void* route, void* stream) {
     if (ctx == nullptr || gating == nullptr) return ADAFUSE_ERR_INVALID_ARG;
     if (h_dtype != ADAFUSE_DTYPE_BF16 && h_dtype != ADAFUSE_DTYPE_F32) return ADAFUSE_ERR_INVALID_ARG;
-    if (T < 0 || d < 4 || (d & 3) != 0 || (ldh & 3) != 0 || ldh < d || !slots_ok(slots))
+    if (T < 0 || d < 4 || d > INT32_MAX || (d & 3) != 0 || (ldh & 3) != 0 || ldh < d || !slots_ok(slots))
         return ADAFUSE_ERR_INVALID_ARG;
     const adafuse_gating& q = *gating;
     const int E = ctx->n_experts;

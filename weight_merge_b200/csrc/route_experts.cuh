@@ -6,15 +6,21 @@
 // every gap it depends on with the bound, and a token with a gap inside it has
 // just the logits concerned summed again, in fp64, and is decided again.
 //
-// Bound: a thread adds 16 products, then chunks of kRouteDepth columns (n on
-// each of C CTAs) in runs of kRouteRun, then runs, 8 warps and the CTAs, so
-// every product passes at most m = 16 + kRouteRun + n / kRouteRun + 1 + 8 + C
-// roundings (16 + n + 8 + C above 32 experts, without runs) and
-//   |z - z64| <= m 2^-24 sum |h w| <= m 2^-24 |h| |w|   (Cauchy-Schwarz).
+// Work: a CTA takes 32 tokens and a share of d; chunks of h (as stored) and of
+// Wr come by cp.async into a ring, and each of 8 warps takes 16 of a chunk's
+// columns: one step of mma.m16n8k16 for two token tiles and every 8 experts.
+// Both factors are split into bf16 terms that add up to them (h: one if it is
+// bf16, else three; Wr: three), so every product is exact, and products below
+// 2^-25 of |h w| are left out.  (On the FP32 units the same sums took twice the
+// instructions, which is what bounds this kernel.)
 //
-// Work: a CTA takes 32 tokens and a share of d.  Chunks of h (as stored) and Wr
-// (rows of E floats are contiguous) come by cp.async into a ring; a warp takes
-// 16 of a chunk's columns, a lane 4 tokens x EMAX / 4 experts of them.
+// Bound: a step's 16 products are summed by the tensor core, which may cut each
+// of 17 addends and the sum at 2^-23 of the largest: 36 units of 2^-24 of the
+// products' magnitude; the smaller terms, the left-out ones and joining them
+// add less than 4.  Steps are added in runs of kRouteRun chunks (n chunks on
+// each of C CTAs), then runs, 8 warps and the CTAs, so with
+// m = 40 + kRouteRun + n / kRouteRun + 1 + 8 + C
+//   |z - z64| <= m 2^-24 sum |h w| <= m 2^-24 |h| |w|   (Cauchy-Schwarz).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -63,9 +69,21 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
         return;
     }
     // scores: softmax over all E, or sigmoid (exp overflows to +inf for very
-    // negative logits, and the score to 0)
+    // negative logits, and the score to 0); in 32 bits where only gates read them
     double s0 = 0.0, s1 = 0.0;
-    if (g.score == ADAFUSE_SCORE_SOFTMAX) {
+    if (g.bias == nullptr && g.n_groups == 1) {
+        const float f0 = (float)z0, f1 = (float)z1;
+        if (g.score == ADAFUSE_SCORE_SOFTMAX) {
+            const double m = warp_max(fmax(in0 ? z0 : kNone, in1 ? z1 : kNone));
+            const float e0 = in0 ? expf((float)(z0 - m)) : 0.f, e1 = in1 ? expf((float)(z1 - m)) : 0.f;
+            const float sum = (float)warp_sum((double)(e0 + e1));
+            s0 = e0 / sum;
+            s1 = e1 / sum;
+        } else {
+            s0 = 1.f / (1.f + expf(-f0));
+            s1 = 1.f / (1.f + expf(-f1));
+        }
+    } else if (g.score == ADAFUSE_SCORE_SOFTMAX) {
         const double m = warp_max(fmax(in0 ? z0 : kNone, in1 ? z1 : kNone));
         s0 = in0 ? exp(z0 - m) : 0.0;
         s1 = in1 ? exp(z1 - m) : 0.0;
@@ -149,12 +167,12 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
         // scores divided by a factor common to the picks, so that the largest
         // stays near 1 where all of them underflow: exp(z - zmax) for softmax;
         // for sigmoid e^min(z,0) / (1 + e^-|z|) without e^min(zmax,0)
-        double x = 0.0;
+        float x = 0.f;
         if (lane < n)
             x = g.score == ADAFUSE_SCORE_SOFTMAX
-                    ? exp(my_z - zmax)
-                    : exp(fmin(my_z, 0.0) - fmin(zmax, 0.0)) / (1.0 + exp(-fabs(my_z)));
-        gate = x / warp_sum(x);
+                    ? expf((float)(my_z - zmax))
+                    : expf((float)(fmin(my_z, 0.0) - fmin(zmax, 0.0))) / (1.f + expf((float)-fabs(my_z)));
+        gate = x / warp_sum((double)x);
     }
     if (lane < g.slots) {
         idx_out[lane] = lane < n ? my_pick : -1;
@@ -167,11 +185,11 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
 // comparison depends on carries a bound of its error, from the logits' (delta)
 // and from its own arithmetic.  Returns the experts whose logits have to be
 // known better before the decision stands (0: it stands, and the record is
-// written).  lo / hi: EMAX floats each of shared memory per token.  All lanes
-// of the warp call it; `valid` marks tokens that exist.
+// written).  ends: 4 * EMAX floats of shared memory per token.  All lanes of
+// the warp call it; `valid` marks tokens that exist.
 template <int EPL>
 __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float delta, const GateParams& g, int sub,
-                                               bool valid, float* lo, float* hi, int32_t* __restrict__ route,
+                                               bool valid, float* ends, int32_t* __restrict__ route,
                                                int64_t t) {
     constexpr uint32_t kAll = 0xffffffffu;
     auto seg_max = [](float v) {
@@ -243,6 +261,7 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
         // a group's worth lies between the sums of its best values' lower and
         // upper ends
         const int per = g.E / g.n_groups;
+        float *lo = ends, *hi = ends + 8 * EPL, *glo = hi + 8 * EPL, *ghi = glo + 8 * EPL;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (e0 + i < g.E) {
@@ -250,48 +269,80 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
                 hi[e0 + i] = on >> i & 1 ? q[i] + eq[i] : -INFINITY;
             }
         __syncwarp();
-        float wl[8], wh[8];   // groups sub, sub + 8, ...
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int grp = sub; grp < g.n_groups; grp += 8) {
             float a = -INFINITY, b = -INFINITY, c = -INFINITY, d = -INFINITY;
-            if (sub + 8 * u < g.n_groups)
-                for (int i = 0; i < per; ++i) {
-                    const float v = lo[(sub + 8 * u) * per + i], w = hi[(sub + 8 * u) * per + i];
-                    if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
-                    if (w > c) { d = c; c = w; } else if (w > d) { d = w; }
-                }
-            wl[u] = g.group_top == 2 && b > -INFINITY ? a + b : a;
-            wh[u] = g.group_top == 2 && d > -INFINITY ? c + d : c;
-            if (fabsf(wl[u]) < INFINITY) wl[u] -= 1.2e-7f * fabsf(wl[u]);
-            if (fabsf(wh[u]) < INFINITY) wh[u] += 1.2e-7f * fabsf(wh[u]);
+            for (int i = grp * per; i < (grp + 1) * per; ++i) {
+                const float v = lo[i], w = hi[i];
+                if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
+                if (w > c) { d = c; c = w; } else if (w > d) { d = w; }
+            }
+            float wl = g.group_top == 2 && b > -INFINITY ? a + b : a;
+            float wh = g.group_top == 2 && d > -INFINITY ? c + d : c;
+            if (fabsf(wl) < INFINITY) wl -= 1.2e-7f * fabsf(wl);
+            if (fabsf(wh) < INFINITY) wh += 1.2e-7f * fabsf(wh);
+            glo[grp] = wl;
+            ghi[grp] = wh;
         }
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (sub + 8 * u < g.n_groups) { lo[sub + 8 * u] = wl[u]; hi[sub + 8 * u] = wh[u]; }
         __syncwarp();
         // a group is kept if fewer than top_groups may come before it, dropped
         // if at least that many must; anything else is open
-        uint64_t keep = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int grp = sub + 8 * u;
-            if (grp >= g.n_groups) continue;
+        unsigned long long keep = 0, unsure = 0;
+        for (int grp = sub; grp < g.n_groups; grp += 8) {
+            const float wl = glo[grp], wh = ghi[grp];
             int may = 0, must = 0;
             for (int i = 0; i < g.n_groups; ++i) {
                 if (i == grp) continue;
                 // a group with nothing enabled is worth -inf exactly
-                may += hi[i] >= wl[u] && (hi[i] > -INFINITY || i < grp);
-                must += lo[i] > wh[u] || (lo[i] == -INFINITY && wh[u] == -INFINITY && i < grp);
+                may += ghi[i] >= wl && (ghi[i] > -INFINITY || i < grp);
+                must += glo[i] > wh || (glo[i] == -INFINITY && wh == -INFINITY && i < grp);
             }
             if (may < g.top_groups) keep |= 1ull << grp;
-            else if (must < g.top_groups) all = true;
+            else if (must < g.top_groups) unsure |= 1ull << grp;
         }
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) keep |= __shfl_xor_sync(kAll, (unsigned long long)keep, off);
+        for (int off = 4; off > 0; off >>= 1) {
+            keep |= __shfl_xor_sync(kAll, keep, off);
+            unsure |= __shfl_xor_sync(kAll, unsure, off);
+        }
+        // of an unsure group, the experts that may be among its best are open
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e0 + i < g.E && !(keep >> ((e0 + i) / per) & 1)) on &= ~(1u << i);
+        for (int i = 0; i < EPL; ++i) {
+            if (e0 + i >= g.E) continue;
+            const int grp = (e0 + i) / per;
+            if (unsure >> grp & 1) {
+                if (on >> i & 1) {
+                    int above = 0;   // experts of the group surely before this one
+                    for (int u = grp * per; u < (grp + 1) * per; ++u) above += lo[u] > q[i] + eq[i];
+                    if (above < g.group_top) open |= 1u << i;
+                }
+            } else if (!(keep >> grp & 1)) {
+                on &= ~(1u << i);
+            }
+        }
+        if (__any_sync(kAll, unsure != 0)) {
+            // which experts the picks choose from depends on the groups: any
+            // two of the kept and unsure groups' that are too close are open
+            __syncwarp();
+            unsigned long long cand = (unsigned long long)on << e0;
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) cand |= __shfl_xor_sync(kAll, cand, off);
+            if (g.bias == nullptr) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (e0 + i < g.E) { lo[e0 + i] = z[i] - delta; hi[e0 + i] = z[i] + delta; }
+            }
+            __syncwarp();
+            if (unsure != 0) {
+#pragma unroll 1
+                for (int u = 0; u < g.E; ++u) {
+                    if (!(cand >> u & 1)) continue;
+                    const float l = lo[u], h = hi[u];
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i)
+                        if ((on >> i & 1) && u != e0 + i && lo[e0 + i] <= h && l <= hi[e0 + i]) open |= 1u << i;
+                }
+            }
+        }
         __syncwarp();
     }
     // k picks, the lower index first among equals (equal keys are open, infinite
@@ -332,7 +383,8 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if ((on >> i & 1) && (g.bias != nullptr ? q[i] + eq[i] : z[i] + delta) >= kb - eb) rivals |= 1u << i;
-        if (best == kMaxExperts || isinf(kb)) rivals = 0;
+        // equal keys that are exact are settled by the index
+        if (best == kMaxExperts || isinf(kb) || (g.bias == nullptr && delta == 0.f)) rivals = 0;
         open |= rivals;
         if (__ballot_sync(kAll, rivals != 0) >> (threadIdx.x & 24) & 0xffu) open |= mine;
         if (best < kMaxExperts) {
@@ -370,20 +422,23 @@ constexpr int kRouteDepth = 128;      // columns of h per chunk, 16 a warp
 constexpr int kRouteStages = 4;
 constexpr int kRouteRun = 6;
 
-// Shared memory of a stage: h rows padded by 16 bytes (their 16-byte pieces
-// fall into different banks), then Wr's rows as they are, 256 bytes of slack for
-// the reads past the last expert.
+// Shared memory of a stage: h rows padded by 16 bytes, then rows of Wr padded to
+// 4 or 12 floats past a multiple of 16, so that fragment reads fall into
+// different banks; 256 bytes of slack for the reads past the last expert.
 template <typename H>
 __host__ __device__ constexpr uint32_t route_h_pitch() { return kRouteDepth * (uint32_t)sizeof(H) + 16; }
+__host__ __device__ constexpr int route_w_pitch(int E) {   // in floats
+    return (E + 3) / 4 * 4 + ((E + 3) / 4 % 2 == 0 ? 4 : 0);
+}
 template <typename H>
 __host__ __device__ constexpr uint32_t route_stage_bytes(int E) {
-    return kRouteTokens * route_h_pitch<H>() + (((uint32_t)kRouteDepth * E * 4 + 256u));
+    return kRouteTokens * route_h_pitch<H>() + (uint32_t)kRouteDepth * route_w_pitch(E) * 4u + 256u;
 }
 // after the loop: warps' partial logits and squares, the CTA's sums, the
 // groups' scratch, the logits in 64 bits; the fp64 pass reuses the start
 template <int EMAX>
 __host__ __device__ constexpr uint32_t route_tail_bytes() {
-    return 4u * ((kRouteWarps + 1) * (kRouteTokens + 1) * (EMAX + 1) + 2 * kRouteTokens * EMAX) + 64u +
+    return 4u * ((kRouteWarps + 1) * (kRouteTokens + 1) * (EMAX + 1) + 4 * kRouteTokens * EMAX) + 64u +
            8u * (kRouteTokens + kRouteWarps) * kMaxExperts;
 }
 
@@ -399,27 +454,75 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Four consecutive values of a row in shared memory as floats.
-__device__ __forceinline__ float4 route_h4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 route_h4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+// Two floats as the sum of packed bf16 terms, largest first (24 bits: exact up
+// to 2^-27 of the value).
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(x, y);
+    x -= __uint_as_float(hi << 16);
+    y -= __uint_as_float(hi & 0xffff0000u);
+    mid = pack_bf16(x, y);
+    lo = pack_bf16(x - __uint_as_float(mid << 16), y - __uint_as_float(mid & 0xffff0000u));
+}
+// d = a b, and d += a b
+__device__ __forceinline__ void route_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void route_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A token tile's 16 columns as A fragments, one plane per term, and the squares
+// of its values added to the lane's two rows.
+__device__ __forceinline__ void route_h_frag(const float* r0, const float* r1, uint32_t (&a)[3][4], float& s0,
+                                             float& s1) {
+    const float2 v[4] = {*reinterpret_cast<const float2*>(r0), *reinterpret_cast<const float2*>(r1),
+                         *reinterpret_cast<const float2*>(r0 + 8), *reinterpret_cast<const float2*>(r1 + 8)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        split3(v[i].x, v[i].y, a[0][i], a[1][i], a[2][i]);
+        float& s = i & 1 ? s1 : s0;
+        s = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, s));
+    }
+}
+__device__ __forceinline__ void route_h_frag(const __nv_bfloat16* r0, const __nv_bfloat16* r1,
+                                             uint32_t (&a)[1][4], float& s0, float& s1) {
+    a[0][0] = *reinterpret_cast<const uint32_t*>(r0);
+    a[0][1] = *reinterpret_cast<const uint32_t*>(r1);
+    a[0][2] = *reinterpret_cast<const uint32_t*>(r0 + 8);
+    a[0][3] = *reinterpret_cast<const uint32_t*>(r1 + 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(a[0][i] << 16), y = __uint_as_float(a[0][i] & 0xffff0000u);
+        float& s = i & 1 ? s1 : s0;
+        s = fmaf(x, x, fmaf(y, y, s));
+    }
 }
 __device__ __forceinline__ float route_load(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float route_load(const __nv_bfloat16* p) {
     return __bfloat162float(__ldg(p));
 }
 
-// VEC: E is a multiple of EMAX / 4 (up to 4), so a lane's experts of a row are
-// read as vectors.  h_piece / w_piece: bytes of a copy (16, or 8 / 4 where rows
-// or Wr are aligned to no more).
-template <int EMAX, bool VEC, typename H>
+// h_piece / w_piece: bytes of a copy (16, or 8 / 4 where rows or Wr are aligned
+// to no more).
+template <int EMAX, typename H>
 __global__ void __launch_bounds__(kRouteThreads, EMAX <= 16 ? 2 : 1)
 route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, const int64_t ldh,
                      const float* __restrict__ Wr, const GateParams g, int32_t* __restrict__ route, const int C,
                      const int h_piece, const int w_piece) {
-    constexpr int TE = EMAX / 4;         // experts per lane
+    constexpr int NT = EMAX / 8;                              // expert tiles
+    constexpr int kTerms = sizeof(H) == 2 ? 1 : 3;            // of h
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = (int)(blockIdx.x % (unsigned)C);
@@ -428,173 +531,142 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     const uint32_t smem_s = (uint32_t)__cvta_generic_to_shared(smem);
     const uint32_t stage_bytes = route_stage_bytes<H>(g.E);
     constexpr uint32_t kPitch = route_h_pitch<H>();
-    const int64_t chunks = (d + kRouteDepth - 1) / kRouteDepth;
+    const int chunks = (int)((d + kRouteDepth - 1) / kRouteDepth);
 
     // Chunk c (of the CTA's: q, q + C, ...) into a stage; columns from d on read
-    // as zero, rows of missing tokens are left alone.  A thread copies pieces
-    // of one row, tid / 8, and every kRouteThreads-th piece of Wr.
+    // as zero, rows of missing tokens are left alone.  A thread copies pieces of
+    // one row, tid / 8, and every kRouteThreads-th piece of Wr, whose places in
+    // the padded rows it works out once.
     const int row = threadIdx.x >> 3;
     const bool row_in = row < ntok;
     const H* hrow = h + (tok0 + (row_in ? row : 0)) * ldh;
     const uint32_t h_dst = smem_s + (uint32_t)row * kPitch;
     const uint32_t w_dst = smem_s + kRouteTokens * kPitch;
-    const int w_all = kRouteDepth * g.E * 4;
-    auto load_chunk = [&](int64_t c, int stage) {
-        if (c < chunks) {
-            const int64_t k0 = c * kRouteDepth;
-            const int cols = (int)(d - k0 < kRouteDepth ? d - k0 : kRouteDepth);
-            const uint32_t so = (uint32_t)stage * stage_bytes;
+    const int w_pitch = route_w_pitch(g.E);
+    const uint32_t w_row = (uint32_t)w_pitch * 4u;
+    const bool vec = h_piece == 16 && w_piece == 16 && (g.E & 3) == 0;
+    const int whole = (int)(d / kRouteDepth);
+    const char* h_src = reinterpret_cast<const char*>(hrow) + (threadIdx.x & 7) * 16;
+    const char* w_src = reinterpret_cast<const char*>(Wr) + threadIdx.x * 16;
+    const int w_chunk = kRouteDepth * g.E * 4;
+    uint32_t w_at[NT];   // piece tid + 256 j: E / 4 pieces a row
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int per = max(g.E >> 2, 1), i = (int)threadIdx.x + j * kRouteThreads;
+        w_at[j] = w_dst + (uint32_t)(i / per) * w_row + (uint32_t)(i % per) * 16u;
+    }
+    auto load_chunk = [&](int c, int stage) {
+        const uint32_t so = (uint32_t)stage * stage_bytes;
+        if (c < whole && vec) {
             if (row_in) {
-                if (h_piece == 16) {
-                    constexpr int kPer = 16 / (int)sizeof(H);
+                const char* src = h_src + (int64_t)c * (kRouteDepth * (int)sizeof(H));
+                const uint32_t dst = h_dst + so + (threadIdx.x & 7) * 16;
 #pragma unroll
-                    for (int k = (threadIdx.x & 7) * kPer; k < kRouteDepth; k += 8 * kPer) {
-                        const int left = (cols - k) * (int)sizeof(H);
-                        cp_async<16>(h_dst + so + k * (uint32_t)sizeof(H), hrow + k0 + (left > 0 ? k : 0),
-                                     left <= 0 ? 0 : left < 16 ? left : 16);
-                    }
-                } else {
-                    constexpr int kPer = 8 / (int)sizeof(H);
+                for (int j = 0; j < kRouteDepth * (int)sizeof(H) / 128; ++j) cp_async<16>(dst + 128 * j, src + 128 * j, 16);
+            }
+            const char* src = w_src + (int64_t)c * w_chunk;
 #pragma unroll
-                    for (int k = (threadIdx.x & 7) * kPer; k < kRouteDepth; k += 8 * kPer) {
-                        const int left = (cols - k) * (int)sizeof(H);
-                        cp_async<8>(h_dst + so + k * (uint32_t)sizeof(H), hrow + k0 + (left > 0 ? k : 0),
-                                    left <= 0 ? 0 : 8);
-                    }
+            for (int j = 0; j < NT; ++j)
+                if ((int)threadIdx.x * 16 + j * (kRouteThreads * 16) < w_chunk)
+                    cp_async<16>(w_at[j] + so, src + j * (kRouteThreads * 16), 16);
+        } else if (c < chunks) {
+            const int64_t k0 = (int64_t)c * kRouteDepth;
+            const int cols = (int)(d - k0 < kRouteDepth ? d - k0 : kRouteDepth);
+            if (row_in) {
+                const int per = h_piece / (int)sizeof(H);
+#pragma unroll 1
+                for (int k = (threadIdx.x & 7) * per; k < kRouteDepth; k += 8 * per) {
+                    const int left = (cols - k) * (int)sizeof(H);
+                    const int valid = left <= 0 ? 0 : left < h_piece ? left : h_piece;
+                    const H* src = hrow + k0 + (left > 0 ? k : 0);
+                    const uint32_t dst = h_dst + so + (uint32_t)k * (uint32_t)sizeof(H);
+                    if (h_piece == 16) cp_async<16>(dst, src, valid); else cp_async<8>(dst, src, valid);
                 }
             }
-            const char* wsrc = reinterpret_cast<const char*>(Wr + k0 * g.E);
-            const int w_in = cols * g.E * 4;   // a multiple of 16
-            if (w_piece == 16) {
-                for (int o = threadIdx.x * 16; o < w_all; o += kRouteThreads * 16)
-                    cp_async<16>(w_dst + so + o, wsrc + (o < w_in ? o : 0), o < w_in ? 16 : 0);
-            } else {
-                for (int o = threadIdx.x * 4; o < w_all; o += kRouteThreads * 4)
-                    cp_async<4>(w_dst + so + o, wsrc + (o < w_in ? o : 0), o < w_in ? 4 : 0);
+            const float* src = Wr + k0 * g.E;
+            const int n = vec ? g.E >> 2 : g.E, floats = vec ? 4 : 1;   // pieces a row
+#pragma unroll 1
+            for (int i = threadIdx.x; i < kRouteDepth * n; i += kRouteThreads) {
+                const int k = i / n, e = i - k * n;
+                const uint32_t dst = w_dst + so + k * w_row + e * floats * 4;
+                const float* from = src + (k < cols ? i * floats : 0);
+                if (vec) cp_async<16>(dst, from, k < cols ? 16 : 0); else cp_async<4>(dst, from, k < cols ? 4 : 0);
             }
         }
         cp_async_commit();
     };
 
-    // lane: tokens tl, tl + 8, tl + 16, tl + 24; experts TE * eg .. + TE
-    const int tl = lane >> 2, eg = lane & 3;
-    // sums of a chunk, of kRouteRun chunks (where registers allow), of all
-    constexpr bool kRuns = EMAX <= 32;
-    float sum[4][TE], run[kRuns ? 4 : 1][TE], hh = 0.f, ww[EMAX > 32 ? 2 : 1];
+    // fragments: lane = 4 * g8 + tig holds tokens 16 m + g8 and + 8, experts
+    // 8 n + 2 tig and + 1
+    const int g8 = lane >> 2, tig = lane & 3;
+    float sum[2][NT][4], run[2][NT][4], hh[2][2], ww[NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        hh[m][0] = hh[m][1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[m][n][i] = run[m][n][i] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ww[n] = 0.f;
     int in_run = 0;
-#pragma unroll
-    for (int i = 0; i < (kRuns ? 4 : 1); ++i)
-#pragma unroll
-        for (int e = 0; e < TE; ++e) run[i][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < TE; ++e) sum[i][e] = 0.f;
-    ww[0] = 0.f;
-    if (EMAX > 32) ww[EMAX > 32 ? 1 : 0] = 0.f;
 
     sm100::pdl_wait();   // set-up overlaps the end of the launch before this one
 #pragma unroll
-    for (int s = 0; s < kRouteStages - 1; ++s) load_chunk(q + (int64_t)s * C, s);
+    for (int s = 0; s < kRouteStages - 1; ++s) load_chunk(q + s * C, s);
     int stage = 0;
 #pragma unroll 1
-    for (int64_t c = q; c < chunks; c += C) {
+    for (int c = q; c < chunks; c += C) {
         cp_async_wait<kRouteStages - 2>();
         __syncthreads();   // the chunk has landed, and the stage before it is free
-        load_chunk(c + (int64_t)(kRouteStages - 1) * C, stage == 0 ? kRouteStages - 1 : stage - 1);
+        load_chunk(c + (kRouteStages - 1) * C, stage == 0 ? kRouteStages - 1 : stage - 1);
         const uint8_t* base = smem + (size_t)stage * stage_bytes;
-        const float* wt = reinterpret_cast<const float*>(base + kRouteTokens * kPitch);
-        float acc[4][TE];
+        const float* wt = reinterpret_cast<const float*>(base + kRouteTokens * kPitch) +
+                          (16 * warp + 2 * tig) * w_pitch + g8;
+        uint32_t a[2][kTerms][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m) {
+            const H* r0 = reinterpret_cast<const H*>(base + (size_t)(16 * m + g8) * kPitch) + 16 * warp + 2 * tig;
+            const H* r1 = reinterpret_cast<const H*>(reinterpret_cast<const uint8_t*>(r0) + 8 * kPitch);
+            route_h_frag(r0, r1, a[m], hh[m][0], hh[m][1]);
+        }
 #pragma unroll
-            for (int e = 0; e < TE; ++e) acc[i][e] = 0.f;
-        // few warps an SM: independent loads in flight rather than short code
-#pragma unroll(EMAX <= 32 ? 4 : 1)
-        for (int k4 = 0; k4 < 16; k4 += 4) {
-            const int k = 16 * warp + k4;
-            float4 x[4];
+        for (int n = 0; n < NT; ++n) {
+            const float* w = wt + 8 * n;
+            const float w0 = w[0], w1 = w[w_pitch], w2 = w[8 * w_pitch], w3 = w[9 * w_pitch];
+            ww[n] = fmaf(w0, w0, fmaf(w1, w1, fmaf(w2, w2, fmaf(w3, w3, ww[n]))));
+            uint32_t b[3][2];
+            split3(w0, w1, b[0][0], b[1][0], b[2][0]);
+            split3(w2, w3, b[0][1], b[1][1], b[2][1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = route_h4(reinterpret_cast<const H*>(base + (size_t)(tl + 8 * i) * kPitch) + k);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const float* wrow = wt + (k + kk) * g.E + TE * eg;
-                float w[TE];
-                if constexpr (VEC && TE == 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(wrow);
-                    w[0] = v.x; w[1] = v.y;
-                } else if constexpr (VEC) {
-#pragma unroll
-                    for (int e = 0; e < TE; e += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(wrow + e);
-                        w[e] = v.x; w[e + 1] = v.y; w[e + 2] = v.z; w[e + 3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < TE; ++e) w[e] = TE * eg + e < g.E ? wrow[e] : 0.f;
+            for (int m = 0; m < 2; ++m) {
+                float z[4];   // the smallest products first
+                route_mma0(z, a[m][0], b[2][0], b[2][1]);
+                if constexpr (kTerms == 3) {
+                    route_mma(z, a[m][2], b[0][0], b[0][1]);
+                    route_mma(z, a[m][1], b[1][0], b[1][1]);
+                    route_mma(z, a[m][1], b[0][0], b[0][1]);
                 }
+                route_mma(z, a[m][0], b[1][0], b[1][1]);
+                route_mma(z, a[m][0], b[0][0], b[0][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float xv = kk == 0 ? x[i].x : kk == 1 ? x[i].y : kk == 2 ? x[i].z : x[i].w;
-#pragma unroll
-                    for (int e = 0; e < TE; ++e) acc[i][e] = fmaf(xv, w[e], acc[i][e]);
-                }
+                for (int i = 0; i < 4; ++i) run[m][n][i] += z[i];
             }
         }
-        if constexpr (kRuns) {
+        if (++in_run == kRouteRun) {
+            in_run = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < TE; ++e) run[i][e] += acc[i][e];
-            if (++in_run == kRouteRun) {
-                in_run = 0;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < TE; ++e) {
-                        sum[i][e] += run[i][e];
-                        run[i][e] = 0.f;
+                    for (int i = 0; i < 4; ++i) {
+                        sum[m][n][i] += run[m][n][i];
+                        run[m][n][i] = 0.f;
                     }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < TE; ++e) sum[i][e] += acc[i][e];
-        }
-        // squares of the same columns, for the bound: lane = token, lane = expert
-        {
-            const H* hr = reinterpret_cast<const H*>(base + (size_t)lane * kPitch) + 16 * warp;
-            float2 a = make_float2(0.f, 0.f), b = a;
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const float4 v = route_h4(hr + k);
-                a.x = fmaf(v.x, v.x, a.x);
-                a.y = fmaf(v.y, v.y, a.y);
-                b.x = fmaf(v.z, v.z, b.x);
-                b.y = fmaf(v.w, v.w, b.y);
-            }
-            hh += (a.x + a.y) + (b.x + b.y);
-#pragma unroll
-            for (int u = 0; u < (EMAX > 32 ? 2 : 1); ++u)
-                if (lane + 32 * u < g.E) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float v = wt[(16 * warp + k) * g.E + lane + 32 * u];
-                        c[k & 3] = fmaf(v, v, c[k & 3]);
-                    }
-                    ww[u] += (c[0] + c[1]) + (c[2] + c[3]);
-                }
         }
         if (++stage == kRouteStages) stage = 0;
-    }
-    if constexpr (kRuns) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < TE; ++e) sum[i][e] += run[i][e];
     }
     cp_async_wait<0>();
     __syncthreads();   // the ring is free
@@ -604,19 +676,35 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     constexpr int kRow = EMAX + 1, kPart = (kRouteTokens + 1) * kRow;
     float* part = reinterpret_cast<float*>(smem);
     float* total = part + kRouteWarps * kPart;
-    float* ends = total + kPart;             // [32][2][EMAX], the groups' scratch
+    float* ends = total + kPart;             // [32][4][EMAX], the groups' scratch
     // the logits in 64 bits [32][64], then the fp64 pass's sums and scratch
     double* fixed = reinterpret_cast<double*>(
-        smem + ((4u * ((kRouteWarps + 1) * kPart + 2 * kRouteTokens * EMAX) + 15u) & ~15u));
+        smem + ((4u * ((kRouteWarps + 1) * kPart + 4 * kRouteTokens * EMAX) + 15u) & ~15u));
     {
         float* mine = part + warp * kPart;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m) {
+            const int t0 = 16 * m + g8;
 #pragma unroll
-            for (int e = 0; e < TE; ++e) mine[(tl + 8 * i) * kRow + TE * eg + e] = sum[i][e];
-        mine[lane * kRow + EMAX] = hh;
-        if (lane < EMAX) mine[kRouteTokens * kRow + lane] = ww[0];
-        if (EMAX > 32) mine[kRouteTokens * kRow + 32 + lane] = ww[EMAX > 32 ? 1 : 0];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mine[(t0 + (i >> 1) * 8) * kRow + 8 * n + 2 * tig + (i & 1)] = sum[m][n][i] + run[m][n][i];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = hh[m][i];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (tig == 0) mine[(t0 + 8 * i) * kRow + EMAX] = v;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float v = ww[n];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (tig == 0) mine[kRouteTokens * kRow + 8 * n + g8] = v;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kPart; i += kRouteThreads) {
@@ -625,23 +713,33 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
         for (int w = 1; w < kRouteWarps; ++w) v += part[w * kPart + i];
         total[i] = v;
     }
-    if (C > 1) sm100::cluster_sync(); else __syncthreads();
-    auto total_at = [&](int i) {
-        if (C == 1) return total[i];
-        float f[8];   // all requested before the first is added
+    // CTA q decides tokens q, q + C, ...: row t / C of zt, then the experts' squares
+    float* zt = total;
+    if (C > 1) {
+        sm100::cluster_sync();
+        zt = part;   // the warps' sums are done with
+        const int rows = kRouteTokens / C, n = (rows + 1) * kRow;
+        for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+            const int r = i / kRow, src = (r < rows ? q + C * r : kRouteTokens) * kRow + i - r * kRow;
+            float f[8];   // all requested before the first is added
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            f[c] = 0.f;
-            if (c < C)
-                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                             : "=f"(f[c])
-                             : "r"(sm100::cluster_addr(&total[i], (uint32_t)c)));
+            for (int c = 0; c < 8; ++c) {
+                f[c] = 0.f;
+                if (c < C)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(f[c])
+                                 : "r"(sm100::cluster_addr(&total[src], (uint32_t)c)));
+            }
+            float v = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v += f[c];
+            zt[i] = v;
         }
-        float v = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v += f[c];
-        return v;
-    };
+        sm100::cluster_sync();   // peers are done with this CTA's sums
+    } else {
+        __syncthreads();
+    }
+    const float* squares = zt + kRouteTokens / C * kRow;
 
     // ---- decisions: CTA q takes tokens q, q + C, ...; eight lanes a token
     constexpr int EPL = EMAX / 8;
@@ -651,23 +749,24 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     float wmax = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        if (sub * EPL + i < g.E) wmax = fmaxf(wmax, total_at(kRouteTokens * kRow + sub * EPL + i));
+        if (sub * EPL + i < g.E) wmax = fmaxf(wmax, squares[sub * EPL + i]);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
     const bool valid = t < ntok;
-    const int tt = valid ? t : 0;
+    const float* zrow = zt + (valid ? t / C : 0) * kRow;
     float z[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) z[i] = sub * EPL + i < g.E ? total_at(tt * kRow + sub * EPL + i) : 0.f;
+    for (int i = 0; i < EPL; ++i) z[i] = sub * EPL + i < g.E ? zrow[sub * EPL + i] : 0.f;
     // 1.02: the squares are fp32 sums themselves; terms below fp32's normal
     // range are off by up to 2^-149 each instead.  (A NaN in Wr shows in z.)
-    const int mine_chunks = (int)((chunks + C - 1) / C);
-    const float roundings = 16.f + kRouteWarps + (float)C +
-                            (kRuns ? kRouteRun + (float)(mine_chunks / kRouteRun + 1) : (float)mine_chunks);
-    const float delta = 1.02f * roundings * 0x1p-24f * sqrtf(total_at(tt * kRow + EMAX)) * sqrtf(wmax) +
-                        (float)d * 0x1p-148f;
-    const uint64_t open = route_decide32<EPL>(z, delta, g, sub, valid, ends + (tt * 2) * EMAX,
-                                              ends + (tt * 2 + 1) * EMAX, route, tok0 + t);
+    const int mine_chunks = (chunks + C - 1) / C;
+    const float roundings = 49.f + kRouteRun + (float)(mine_chunks / kRouteRun) + (float)C;
+    // A router of zeros (as they are initialised) is exact.
+    const float delta = wmax == 0.f ? 0.f
+                                    : 1.02f * roundings * 0x1p-24f * sqrtf(zrow[EMAX]) * sqrtf(wmax) +
+                                          (float)d * 0x1p-148f;
+    const uint64_t open = route_decide32<EPL>(z, delta, g, sub, valid,
+                                              ends + (threadIdx.x >> 3) * 4 * EMAX, route, tok0 + t);
     if (valid) {
         if (sub == 0) open_s[t] = open;
         if (open != 0) {
@@ -676,59 +775,64 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
                 if (sub * EPL + i < g.E) fixed[t * kMaxExperts + sub * EPL + i] = (double)z[i];
         }
     }
-    if (C > 1) sm100::cluster_sync();   // peers may still read this CTA's sums
     if (!__syncthreads_or(valid && open != 0)) return;
 
-    // ---- what the bounds left open, in fp64: for each token the CTA sums the
-    // logits of four neighbouring experts at a time, a thread every 256th
-    // column (16 of them requested at once), then its warps decide again
-    double* sums = reinterpret_cast<double*>(smem);   // [8 warps][4]
-    const bool w_vec = w_piece == 16 && (g.E & 3) == 0;
+    // ---- what the bounds left open, in fp64: for each token the CTA sums two
+    // open logits at a time (most often there are two), a thread every 256th
+    // column, eight of them requested at once; then its warps decide again
+    double* sums = reinterpret_cast<double*>(smem);   // [8 warps][2]
     for (int u = q; u < ntok; u += C) {
-        const uint64_t rest = open_s[u];
+        uint64_t rest = open_s[u];
         const H* hu = h + (tok0 + u) * ldh;
-        for (int e = 0; e < g.E; e += 4) {
-            if ((rest >> e & 15u) == 0) continue;
-            double a[4] = {0.0, 0.0, 0.0, 0.0};
+        while (rest != 0) {
+            const int ea = __ffsll((long long)rest) - 1;
+            rest &= rest - 1;
+            const int eb = rest != 0 ? __ffsll((long long)rest) - 1 : ea;
+            rest &= rest - 1;
+            double a = 0.0, b = 0.0;
+            const H* px = hu + threadIdx.x;
+            const float *pa = Wr + (int64_t)threadIdx.x * g.E + ea, *pb = pa + (eb - ea);
+            const int w_step = kRouteThreads * g.E;
+            int left = (int)((d - threadIdx.x + kRouteThreads - 1) / kRouteThreads);   // columns of this thread
 #pragma unroll 1
-            for (int64_t i = threadIdx.x; i < d; i += 16 * kRouteThreads) {
-                float x[16];
-                float4 w[16];
+            for (; left >= 8; left -= 8) {
+                float x[8], wa[8], wb[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int64_t k = i + j * kRouteThreads;
-                    const float* src = Wr + k * g.E + e;
-                    x[j] = 0.f;
-                    w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k < d) {
-                        x[j] = route_load(hu + k);
-                        if (w_vec) {
-                            w[j] = __ldg(reinterpret_cast<const float4*>(src));
-                        } else {
-                            w[j].x = __ldg(src);
-                            if (e + 1 < g.E) w[j].y = __ldg(src + 1);
-                            if (e + 2 < g.E) w[j].z = __ldg(src + 2);
-                            if (e + 3 < g.E) w[j].w = __ldg(src + 3);
-                        }
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = route_load(px + j * kRouteThreads);
+                    wa[j] = __ldg(pa);
+                    wb[j] = __ldg(pb);
+                    pa += w_step;
+                    pb += w_step;
                 }
+                px += 8 * kRouteThreads;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const double xv = (double)x[j];
-                    a[0] = fma(xv, (double)w[j].x, a[0]);
-                    a[1] = fma(xv, (double)w[j].y, a[1]);
-                    a[2] = fma(xv, (double)w[j].z, a[2]);
-                    a[3] = fma(xv, (double)w[j].w, a[3]);
+                for (int j = 0; j < 8; ++j) {
+                    a = fma((double)x[j], (double)wa[j], a);
+                    b = fma((double)x[j], (double)wb[j], b);
                 }
             }
+#pragma unroll 1
+            for (; left > 0; --left) {
+                const double x = (double)route_load(px);
+                a = fma(x, (double)__ldg(pa), a);
+                b = fma(x, (double)__ldg(pb), b);
+                px += kRouteThreads;
+                pa += w_step;
+                pb += w_step;
+            }
+            // both sums over the warp: lane 0 ends with a, lane 16 with b
+            const bool up = lane & 16;
+            double r = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) a[v] = warp_sum(a[v]);
-            if (lane < 4) sums[warp * 4 + lane] = lane == 0 ? a[0] : lane == 1 ? a[1] : lane == 2 ? a[2] : a[3];
+            for (int off = 8; off > 0; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+            if ((lane & 15) == 0) sums[warp * 2 + (lane >> 4)] = r;
             __syncthreads();
-            if (threadIdx.x < 4 && e + (int)threadIdx.x < g.E) {
+            if (threadIdx.x < 2) {
                 double v = 0.0;
-                for (int w = 0; w < kRouteWarps; ++w) v += sums[w * 4 + threadIdx.x];
-                fixed[u * kMaxExperts + e + threadIdx.x] = v;
+#pragma unroll
+                for (int w = 0; w < kRouteWarps; ++w) v += sums[w * 2 + threadIdx.x];
+                fixed[u * kMaxExperts + (threadIdx.x == 0 ? ea : eb)] = v;
             }
             __syncthreads();
         }
