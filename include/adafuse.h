@@ -526,8 +526,9 @@ typedef struct adafuse_gating {
  * a logit that is not a finite fp32 number gets an empty record.
  * h: [T, d] of h_dtype (ADAFUSE_DTYPE_*), rows ldh elements apart, 16-byte
  * aligned, d and ldh multiples of 4, ldh >= d.  Wr: [d, E] fp32, 4-byte
- * aligned.  route: 16-byte aligned.  E comes from the context.  T == 0 is a
- * no-op.  One launch on `stream`. */
+ * aligned.  d below 2^31.  route: 16-byte aligned.  E comes from the context.
+ * T == 0 is a no-op.  One launch on `stream`.  Tokens with equal or nearly
+ * equal logits cost more (tens of microseconds a token where all 64 tie). */
 ADAFUSE_API int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int64_t T,
                                       int64_t d, int64_t ldh, const float* Wr,
                                       const adafuse_gating* gating, int32_t slots, void* route,
@@ -575,11 +576,14 @@ typedef struct adafuse_linear_args {
 /* y = residual + mul * act(x W^T + bias).  T == 0 is a no-op.  INVALID_ARG
  * for a bad pointer, stride, layer, target or enum, or for
  * ADAFUSE_WEIGHT_BASE without a registered base; UNSUPPORTED_SHAPE for T
- * above 2^31 - 1.  One launch on `stream`. */
+ * above 2^31 - 1.  One launch on `stream` per 2^17 tokens.  The tensor-core
+ * kernels bound every wait; a launch whose wait runs out (1 s) raises
+ * ADAFUSE_STATUS_TIMEOUT and leaves y incomplete. */
 ADAFUSE_API int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stream);
 
 /* Bytes of device workspace adafuse_linear_routed needs for T tokens on this
- * weight (a multiple of 256; not decreasing in T).  Host-only. */
+ * weight (a multiple of 256; not decreasing in T, and the same from 2^17 tokens
+ * on: longer calls work through the tokens in parts).  Host-only. */
 ADAFUSE_API int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, int32_t target,
                                          int64_t T, int32_t io_dtype, int64_t* bytes);
 
@@ -591,7 +595,11 @@ ADAFUSE_API int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, 
  * whose gate is not finite raises ADAFUSE_STATUS_BAD_EXPERT / _BAD_GATE and
  * counts as empty.  x A_e^T is accumulated in fp32; for ADAFUSE_DTYPE_BF16
  * outputs its gated values may be carried as bf16, for ADAFUSE_DTYPE_F32 as
- * two bf16 terms (relative 2^-17).  W is not changed.
+ * two bf16 terms (relative 2^-17).  W is not changed.  A and B hold finite
+ * values: an infinity or NaN in an expert's B may reach tokens that did not
+ * choose it (x may hold anything: a token's row affects that token only).  For
+ * ranks below 8 B is read as the switches read it: adafuse_refresh_adapters
+ * after changing it in place.
  * workspace: 256-byte aligned device memory of at least
  * adafuse_linear_workspace bytes (INVALID_ARG otherwise); calls that may
  * overlap on the GPU need workspaces of their own.  Its contents before and

@@ -226,6 +226,56 @@ def test_route_experts_top2_picks_what_pregate_picks():
     torch.testing.assert_close(a[:, 2:].view(F32), b[:, 2:].view(F32), rtol=1e-5, atol=0)
 
 
+@pytest.mark.parametrize("E", [8, 48, 64])
+@pytest.mark.parametrize("T", [1, 70])
+def test_route_zero_router(T, E):
+    """A router before its first update: every logit 0, so the order is the
+    index's, or the bias's."""
+    d = 1032
+    _, sw = model(8, 8, E=E)
+    g = gen(2)
+    h, Wr = rows(g, T, d, BF), torch.zeros((d, E), device="cuda")
+    bias = torch.randn((E,), generator=g, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        idx, _ = route_check(sw, h, Wr, 8, score=score, k=8)
+        assert np.array_equal(idx, np.tile(np.arange(8), (T, 1)))
+        route_check(sw, h, Wr, 8, score=score, k=8, bias=bias)
+        route_check(sw, h, Wr, 4, score=score, k=4, n_groups=4, top_groups=2, group_top=2)
+        route_check(sw, h, Wr, 4, score=score, k=4, n_groups=4, top_groups=3, group_top=2, bias=bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_next_to_a_border(score):
+    """Groups whose worth differs in the last bits of their columns only, and
+    whose members are far apart."""
+    T, d, E, G = 130, 2052, 32, 4
+    _, sw = model(8, 8, E=E)
+    g = gen(9)
+    h = rows(g, T, d, F32)
+    base = torch.randn((d, E // G), generator=g, device="cuda") * 0.05
+    step = torch.randint(-1, 2, (d, E), generator=g, device="cuda").float() * 2.0 ** -23
+    Wr = (base.repeat(1, G) * (1 + step)).contiguous()
+    for top in (1, 2, 3):
+        for gt in (1, 2):
+            route_check(sw, h, Wr, 8, score=score, k=8, n_groups=G, top_groups=top, group_top=gt)
+            route_check(sw, h, Wr, 4, score=score, k=3, n_groups=G, top_groups=top, group_top=gt,
+                        bias=torch.zeros(E, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [1, 9, 100])
+@pytest.mark.parametrize("d", [4, 60, 124, 132, 380, 1028])
+@pytest.mark.parametrize("E", [5, 37, 63])
+def test_route_any_alignment(T, d, E):
+    """Wr on a 4-byte boundary with rows of any length, h with rows that no
+    16-byte vector divides, and a short last part of d."""
+    _, sw = model(8, 8, E=E)
+    g = gen(T + d)
+    Wr = (torch.randn((d * E + 1,), generator=g, device="cuda") * 0.05)[1:].view(d, E)
+    assert Wr.data_ptr() % 8 == 4
+    for dtype in (BF, F32):
+        route_check(sw, rows(g, T, d, dtype, pad=4), Wr, 8, score="sigmoid", k=min(E, 8))
+
+
 def test_route_refusals():
     _, sw = model(8, 8, E=8)
     h = torch.zeros((4, 64), device="cuda")
@@ -240,7 +290,7 @@ def test_route_refusals():
         return L.adafuse_route_experts(sw.ctx, h, dt, T, d, ldh, Wr, ctypes.byref(g), slots, route, stream())
 
     for bad in (dict(h=None), dict(h=h.data_ptr() + 4), dict(dt=2), dict(dt=-1), dict(T=-1), dict(d=62),
-                dict(d=0), dict(ldh=60), dict(ldh=66), dict(Wr=None), dict(Wr=Wr.data_ptr() + 2),
+                dict(d=0), dict(d=2 ** 31, ldh=2 ** 31), dict(ldh=60), dict(ldh=66), dict(Wr=None), dict(Wr=Wr.data_ptr() + 2),
                 dict(slots=3), dict(slots=16), dict(slots=0), dict(route=None), dict(route=rt.data_ptr() + 8),
                 dict(score=2), dict(k=0), dict(k=9), dict(slots=2, k=3), dict(n_groups=3), dict(n_groups=0),
                 dict(n_groups=16), dict(n_groups=2, top_groups=3), dict(top_groups=0), dict(group_top=0),
@@ -582,6 +632,112 @@ def test_offsets_past_32_bits():
     sw.linear_routed(0, 0, x, rt, y, workspace(sw, T, False), residual=x.new_zeros((T, out)), stream=stream())
     torch.cuda.synchronize()
     check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0))
+
+
+# More tokens than small tiles serve well: every width a tile of 256 tokens
+# takes, ends of tiles in tokens and columns, contractions with a tail, of one
+# accumulation and of several, and every layout of the adapters' ranks.
+WIDE = [
+    # T, in, out, E, r
+    (2048, 128, 1296, 8, 8), (2047, 200, 1440, 5, 16), (1900, 72, 1584, 3, 32), (1793, 264, 1720, 4, 64),
+    (2030, 136, 1872, 16, 24), (1801, 64, 2008, 8, 5), (1290, 128, 3360, 64, 8), (2041, 192, 2040, 7, 12),
+    (1025, 1608, 4104, 4, 16), (2000, 3208, 2048, 2, 40),
+]
+
+
+@pytest.mark.parametrize("T,inn,out,E,r", WIDE)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_tokens(T, inn, out, E, r, dtype):
+    m, sw = model(out, inn, E=E, r=r, seed=T)
+    g = gen(T + inn)
+    x = rows(g, T, inn, BF, pad=16)
+    k = min(E, 2)
+    rt = make_routes(g, T, E, k, 2, 0.1)
+    kw = dict(bias=torch.randn((out,), generator=g, device="cuda"), mul=rows(g, T, out, dtype, pad=8),
+              residual=rows(g, T, out, dtype))
+    full = torch.full((T + 1, out + 16), 3.0, dtype=dtype, device="cuda")
+    y = full[:T, :out]
+    sw.linear(0, 0, x, y, activation=ACT["gelu"], stream=stream(), **kw)
+    torch.cuda.synchronize()
+    assert (full[:, out:] == 3).all() and (full[T] == 3).all()
+    check(y, *ref.product(x, m.W[0], activation="gelu", out_dtype=dtype, **kw))
+    ws = workspace(sw, T, dtype == F32)
+    guard = torch.full((ws.numel() + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    sw.linear_routed(0, 0, x, rt, y, guard[:ws.numel()], stream=stream(), residual=kw["residual"])
+    torch.cuda.synchronize()
+    assert (full[:, out:] == 3).all() and (full[T] == 3).all() and (guard[ws.numel():] == 0x5a).all()
+    check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0, out_dtype=dtype,
+                          residual=kw["residual"]))
+    assert sw.status(stream()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_tokens_than_one_launch_takes(dtype):
+    T, inn, out, E, r = 2 ** 17 + 21, 64, 72, 4, 8
+    m, sw = model(out, inn, E=E, r=r, seed=2)
+    g = gen(1)
+    x, rt = rows(g, T, inn, BF, pad=8), make_routes(g, T, E, 2, 4, 0.1)
+    kw = dict(mul=rows(g, T, out, dtype, pad=8), residual=rows(g, T, out, dtype))
+    full = torch.full((T, out + 8), 3.0, dtype=dtype, device="cuda")
+    y = full[:, :out]
+    sw.linear(0, 0, x, y, stream=stream(), **kw)
+    torch.cuda.synchronize()
+    check(y, *ref.product(x, m.W[0], out_dtype=dtype, **kw))
+    f32 = dtype == F32
+    assert sw.linear_workspace(0, 0, T, f32) == sw.linear_workspace(0, 0, 2 ** 17, f32)
+    sw.linear_routed(0, 0, x, rt, y, workspace(sw, T, f32), stream=stream(), **kw)
+    torch.cuda.synchronize()
+    assert (full[:, out:] == 3).all()
+    check(y, *ref.product(x, m.W[0], routes=rt, slots=4, A=m.A[0], B=m.B[0], s=2.0, out_dtype=dtype, **kw))
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("r", [4, 8, 12])
+def test_adapters_changed_in_place(T, r):
+    inn, out, E = 256, 264, 4
+    m, sw = model(out, inn, E=E, r=r, seed=3)
+    g = gen(8)
+    x, rt = rows(g, T, inn), make_routes(g, T, E, 2, 2)
+    y, ws = torch.empty((T, out), dtype=BF, device="cuda"), workspace(sw, T, False)
+    for f in (1.0, -2.0):
+        m.A[0].mul_(f)
+        m.B[0].mul_(0.5 * f)
+        Bnd.adafuse_refresh_adapters(sw.ctx, stream())
+        sw.linear_routed(0, 0, x, rt, y, ws, stream=stream())
+        torch.cuda.synchronize()
+        check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0))
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_two_graphs_at_once(T):
+    """Two captured calls with workspaces of their own, replayed on two streams
+    together, on inputs that change between replays."""
+    inn, out, E, r = 1024, 512, 8, 8
+    m, sw = model(out, inn, E=E, r=r, seed=3)
+    jobs = []
+    for i in range(2):
+        x = torch.empty((T, inn), dtype=BF, device="cuda")
+        rt = make_routes(gen(i), T, E, 2, 2)
+        y, ws, st = torch.empty((T, out), dtype=F32, device="cuda"), workspace(sw, T, True), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(3):
+                sw.linear_routed(0, 0, x, rt, y, ws, stream=torch.cuda.current_stream().cuda_stream)
+        jobs.append((st, graph, x, rt, y))
+    for seed in (5, 6):
+        for i, (_, _, x, rt, _) in enumerate(jobs):
+            x.copy_(torch.randn((T, inn), generator=gen(seed + 10 * i), device="cuda"))
+            rt.copy_(make_routes(gen(seed + 20 * i), T, E, 2, 2))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for st, graph, *_ in jobs:
+                with torch.cuda.stream(st):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, _, x, rt, y in jobs:
+            check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0, out_dtype=F32))
+    assert sw.status(stream()) == 0
 
 
 def test_linear_refusals():

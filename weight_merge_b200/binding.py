@@ -386,15 +386,16 @@ def _need(t, dtype: str, what: str) -> None:
         raise ValueError(f"{what}: the last dimension must be contiguous")
 
 
-def _rows(t, dtype, T: int, n: int, what: str):
-    """(address, elements between row starts) of a [T, n] device tensor whose
-    rows are contiguous.  On the decode path: few attribute reads."""
+def _rows(t, dtype, T: int, n: int, device: int, what: str):
+    """(address, elements between row starts) of a [T, n] tensor on the
+    context's device whose rows are contiguous.  On the decode path: few
+    attribute reads."""
     if t.dtype is not dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
     if t.shape != (T, n):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(T, n)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: not on a CUDA device")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, the context is on cuda:{device}")
     ld, unit = t.stride()
     if unit != 1 and n > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
@@ -425,6 +426,7 @@ class Switcher:
         self.desc = make_desc(n_layers, n_targets, n_experts, rank, alpha, ts)
         self.n_layers = n_layers
         self._lib = lib()   # the per-token calls go straight to it
+        self._device = int(device)
         self.ctx = adafuse_create(self.desc, device)
 
     @staticmethod
@@ -498,15 +500,16 @@ class Switcher:
         h_dtype = types.get(h.dtype)
         if h_dtype is None:
             raise TypeError(f"h: dtype {h.dtype}, expected bfloat16 or float32")
-        hp, ldh = _rows(h, h.dtype, T, d, "h")
+        hp, ldh = _rows(h, h.dtype, T, d, self._device, "h")
         E = self.desc.n_experts
-        wp, ldw = _rows(Wr, self._f32, d, E, "Wr")
+        wp, ldw = _rows(Wr, self._f32, d, E, self._device, "Wr")
         if ldw != E:
             raise ValueError("Wr: rows must be contiguous")
-        if gating._keep is not None and gating._keep.numel() != E:
-            raise ValueError(f"bias: {gating._keep.numel()} values for {E} experts")
+        bias = gating._keep
+        if bias is not None and (bias.numel() != E or bias.get_device() != self._device):
+            raise ValueError(f"bias: {bias.numel()} values on {bias.device} for {E} experts")
         slots = routes.shape[-1] // 2
-        rp, ldr = _rows(routes, self._i32, T, 2 * slots, "routes")
+        rp, ldr = _rows(routes, self._i32, T, 2 * slots, self._device, "routes")
         if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of h")
         code = self._lib.adafuse_route_experts(self.ctx, hp, h_dtype, T, d, ldh, wp,
@@ -523,15 +526,18 @@ class Switcher:
         io = self._types.get(dtype)
         if io is None:
             raise TypeError(f"y: dtype {dtype}, expected bfloat16 or float32")
-        xp, ldx = _rows(x, self._bf16, T, inn, "x")
-        yp, ldy = _rows(y, dtype, T, out, "y")
-        mp, ldm = (None, 0) if mul is None else _rows(mul, dtype, T, out, "mul")
-        rp, ldr = (None, 0) if residual is None else _rows(residual, dtype, T, out, "residual")
+        dev = self._device
+        xp, ldx = _rows(x, self._bf16, T, inn, dev, "x")
+        yp, ldy = _rows(y, dtype, T, out, dev, "y")
+        mp, ldm = (None, 0) if mul is None else _rows(mul, dtype, T, out, dev, "mul")
+        rp, ldr = (None, 0) if residual is None else _rows(residual, dtype, T, out, dev, "residual")
         bp = None
         if bias is not None:
             if bias.shape != (out,):
                 raise ValueError(f"bias: shape {tuple(bias.shape)}, expected {(out,)}")
             _need(bias, "float32", "bias")
+            if bias.get_device() != dev:
+                raise ValueError(f"bias: on {bias.device}, the context is on cuda:{dev}")
             bp = bias.data_ptr()
         return LinearArgs(layer, target, ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT,
                           activation, io, T, xp, ldx, bp, mp, ldm, rp, ldr, yp, ldy)
@@ -558,11 +564,11 @@ class Switcher:
         linear_workspace() bytes that no overlapping call uses."""
         a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
         slots = routes.shape[-1] // 2
-        rp, ldr = _rows(routes, self._i32, a.T, 2 * slots, "routes")
+        rp, ldr = _rows(routes, self._i32, a.T, 2 * slots, self._device, "routes")
         if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of x")
-        if not workspace.is_cuda:
-            raise ValueError("workspace: not on a CUDA device")
+        if workspace.get_device() != self._device:
+            raise ValueError(f"workspace: on {workspace.device}")
         code = self._lib.adafuse_linear_routed(self.ctx, ctypes.byref(a), rp, slots,
                                                workspace.data_ptr(), workspace.nbytes, stream or None)
         if code:

@@ -28,9 +28,28 @@ const PairDesc* find_pair(const adafuse_ctx* ctx, int32_t layer, int32_t target)
 }
 
 // A [T, n] operand of `size`-byte elements with rows ld apart: 16-byte aligned
-// base, rows whole multiples of 16 bytes, at least n long.
+// base, rows whole multiples of 16 bytes, at least n long, less than 2^40 bytes
+// apart (the reach of a tensor map).
 bool rows_ok(const void* p, int64_t ld, int64_t n, int64_t size) {
-    return p != nullptr && aligned16(p) && ld >= n && ld <= INT64_MAX / 16 && ld * size % 16 == 0;
+    return p != nullptr && aligned16(p) && ld >= n && ld < ((int64_t)1 << 40) / size && ld * size % 16 == 0;
+}
+
+// Tokens of one launch: tile coordinates stay far inside 32 bits, and a routed
+// product's second launch, whose waits are bounded, never waits long for its
+// first.
+constexpr int64_t kTokensPerLaunch = (int64_t)1 << 17;
+
+// The parameters of n tokens from the t0-th on.
+LinearParams token_range(const LinearParams& p, int64_t t0, int64_t n) {
+    LinearParams q = p;
+    const int64_t size = p.f32 ? 4 : 2;
+    q.T = n;
+    q.x = p.x + t0 * p.ldx;
+    if (p.mul != nullptr) q.mul = static_cast<const char*>(p.mul) + t0 * p.ldmul * size;
+    if (p.res != nullptr) q.res = static_cast<const char*>(p.res) + t0 * p.ldres * size;
+    q.y = static_cast<char*>(p.y) + t0 * p.ldy * size;
+    if (p.routes != nullptr) q.routes = p.routes + t0 * 2 * p.slots;
+    return q;
 }
 
 // Checks of a product's arguments, and its launch parameters.
@@ -147,12 +166,17 @@ int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stre
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    TcLinear L;
-    std::memset(&L, 0, sizeof L);
-    L.p = p;
-    const cudaError_t e = p.T <= kStreamMaxTokens
-                              ? launch_stream<kProduct>(p, p.W, p.out, nullptr, ctx, s)
-                              : launch_product(L, ctx, s);
+    cudaError_t e = cudaSuccess;
+    if (p.T <= kStreamMaxTokens) {
+        e = launch_stream<kProduct>(p, p.W, p.out, nullptr, ctx, s);
+    } else {
+        TcLinear L;
+        std::memset(&L, 0, sizeof L);
+        for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
+            L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
+            e = launch_product(L, ctx, s);
+        }
+    }
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "linear launch");
 }
 
@@ -163,7 +187,7 @@ int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, int32_t targ
     if (pd == nullptr) return ADAFUSE_ERR_INVALID_ARG;
     if (io_dtype != ADAFUSE_DTYPE_BF16 && io_dtype != ADAFUSE_DTYPE_F32) return ADAFUSE_ERR_INVALID_ARG;
     if (T > INT32_MAX) return ADAFUSE_ERR_UNSUPPORTED_SHAPE;
-    *bytes = routed_layout(ctx, *pd, T, io_dtype == ADAFUSE_DTYPE_F32).bytes;
+    *bytes = routed_layout(ctx, *pd, std::min(T, kTokensPerLaunch), io_dtype == ADAFUSE_DTYPE_F32).bytes;
     return ADAFUSE_OK;
 }
 
@@ -176,7 +200,7 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     if (p.T == 0) return ADAFUSE_OK;
     if (routes == nullptr || !aligned16(routes)) return ADAFUSE_ERR_INVALID_ARG;
     const PairDesc* pd = find_pair(ctx, args->layer, args->target);
-    const RoutedLayout lay = routed_layout(ctx, *pd, p.T, p.f32 != 0);
+    const RoutedLayout lay = routed_layout(ctx, *pd, std::min(p.T, kTokensPerLaunch), p.f32 != 0);
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < lay.bytes)
         return ADAFUSE_ERR_INVALID_ARG;
@@ -211,12 +235,15 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
         pad_b_kernel<<<grid, 256, 0, s>>>(p.B, padded, nrows, p.r, lay.rp);
         p.B = padded;
     }
-    L.p = p;
     L.bsteps = (int)ceil_div((int64_t)p.E * lay.rp, 64);
-    L.vsteps = L.terms * L.bsteps;
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_down(L, ctx, s);
-    if (e == cudaSuccess) e = launch_product(L, ctx, s);
+    for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
+        L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
+        L.vsteps = 0;
+        e = launch_down(L, ctx, s);
+        L.vsteps = L.terms * L.bsteps;
+        if (e == cudaSuccess) e = launch_product(L, ctx, s);
+    }
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "routed linear launch");
 }
 

@@ -42,7 +42,8 @@ inline bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t 
 inline bool encode_v(CUtensorMap* m, const TcLinear& L, int box_rows) {
     const int64_t width = (int64_t)L.p.E * L.rp;
     const cuuint64_t dim[3] = {(cuuint64_t)width, (cuuint64_t)L.p.T, (cuuint64_t)L.terms};
-    const cuuint64_t stride[2] = {(cuuint64_t)width * 2, (cuuint64_t)(L.p.T * width * 2)};
+    // (one term: any legal stride, the third coordinate stays 0)
+    const cuuint64_t stride[2] = {(cuuint64_t)width * 2, (cuuint64_t)((L.terms > 1 ? L.p.T : 1) * width * 2)};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     return encode_map(m, 3, L.v, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
