@@ -11,12 +11,13 @@
 // comes from memory once and x stays in L2.  BN is a launch parameter (a
 // multiple of 16): the host takes the width whose tiles fill whole rounds.
 //
-// F32 (fp32 outputs, V of two terms): tensor-core accumulators drop low bits on every
-// 16-deep step (measured: 4e-6 of the result after 4096 products, 1.2e-5 after
-// 11008), so the contraction is cut into chunks of at most kChunkSteps steps,
-// each started from zero, and the epilogue adds them in registers in fp32 (about
-// 0.5 us a chunk of the tensor cores' time; 1.4e-6 of the result is left).  A
-// bf16 output does not see the difference and takes one chunk.
+// F32 (fp32 outputs, V of two terms): tensor-core accumulators drop low bits on
+// every 16-deep piece (1e-6 of the result after 64, more in proportion), so the
+// contraction is cut into chunks of at most kChunkSteps steps, each started from
+// zero, and the epilogue adds them in registers in fp32.  7e-7 of the result is
+// left; chunks of 24 steps left 1.4e-6 and took 301 instead of 308 us for T =
+// 4096, 4096 -> 4096 with 8 experts of rank 8.  A bf16 output does not see the
+// difference and takes one chunk.
 //
 // Routed products: after x and W come V and the stacked B, as in
 // linear_skinny.cuh; kDown writes V (F32: as two terms).
@@ -35,7 +36,7 @@ constexpr int kPairThreads = 640;
 constexpr int kPairEpiWarps = 16;
 constexpr int kPairTokens = 256;
 constexpr int kPairMaxCols = 256;
-constexpr int kChunkSteps = 24;
+constexpr int kChunkSteps = 12;
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairXBytes = 128 * 128;
 constexpr uint32_t kPairStageBytes = 2 * kPairXBytes;   // x, then up to 128 rows of W

@@ -14,8 +14,11 @@
 // the other, and joins them in registers with fp32 additions, for two reasons:
 // successive MMAs on one accumulator wait for each other (about 130 clocks,
 // whatever the width: a 64-column step took 0.28 us on one), and accumulators
-// drop low bits on every piece (measured: 4e-6 of the result after 4096
-// products, 1.2e-5 after 11008).
+// drop low bits on every piece (1e-6 of the result after 64 pieces, more in
+// proportion).  For fp32 outputs (and V of two terms) the accumulators are
+// emptied and started again after at most kFinePieces pieces each: 7e-7 of the
+// result instead of 6e-6 at T = 128, 11008 -> 11008, for 23.2 instead of 22.2 us
+// at T = 64, 4096 -> 11008.  A bf16 output does not see the difference.
 //
 // Routed products append the adapters to the contraction: after the columns of
 // x come those of V [T, E * rp] (every token's gated x A^T, zero for experts it
@@ -49,6 +52,7 @@ struct TcLinear {
 };
 
 constexpr int kSkinnyThreads = 384;
+constexpr int kFinePieces = 48;    // see the file's head
 
 // Wait, as a whole warp, for the phase with the given parity of the barrier at
 // shared-memory address `bar`; gives up (for all lanes alike) after `limit`
@@ -284,7 +288,7 @@ struct SkinnyConfig {
     static constexpr int stages(int ctas) {
         return (int)((ctas == 1 ? 216u * 1024u : 108u * 1024u) / kStageBytes);
     }
-    static constexpr uint32_t smem_bytes(int stages) { return 1024 + stages * kStageBytes + 8 * (2 * stages + 1) + 16; }
+    static constexpr uint32_t smem_bytes(int stages) { return 1024 + stages * kStageBytes + 8 * (2 * stages + 2) + 16; }
     static_assert(TN * 128 * 4 + 32 <= stages_min() * kStageBytes, "the partial tile reuses the ring");
     static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 };
@@ -303,7 +307,8 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * C::kStageBytes);
     uint64_t* empty = full + stages;
     uint64_t* acc_full = empty + stages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* acc_empty = acc_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -314,7 +319,11 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     const int nsteps = L.xsteps + L.vsteps;
     const int k0 = (int)((int64_t)q * nsteps / S), k1 = (int)((int64_t)(q + 1) * nsteps / S);
     const int n = k1 - k0;
-    const int naccs = 4 * n < C::kAccs ? 4 * n : C::kAccs;
+    // even chunks of at most kFinePieces pieces an accumulator
+    constexpr int kChunk = kFinePieces * C::kAccs / 4;
+    const bool fine = MODE == kDown ? L.terms == 2 : L.p.f32 != 0;
+    const int chunks = fine ? (n + kChunk - 1) / kChunk : 1;
+    const int chunk_steps = (n + chunks - 1) / chunks;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -322,6 +331,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             mbar_init(&empty[i], 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 8);        // the warps that read the accumulators
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -365,7 +375,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
         const uint32_t ring_s = smem_u32(ring), full_s = smem_u32(full), empty_s = smem_u32(empty);
         const uint64_t dw = row_desc(ring_s), dx = row_desc(ring_s + C::kWBytes);
         const StepDesc db = b_desc(L, ring_s, 128);
-        int st = 0, i = 0;
+        int st = 0, i = 0;              // i: the step within its chunk
         uint32_t ph = 0, off = 0;       // off: the stage's offset in 16-byte units
         bool ok = true;
         // successive MMAs go to different accumulators (see the file's head)
@@ -381,79 +391,90 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             off += C::kStageBytes / 16;
             if (st == stages) { st = 0; off = 0; ph ^= 1; }
         };
-        const int nx = (k1 < L.xsteps ? k1 : L.xsteps) - k0;   // steps of x and W (<= 0: none)
+        uint32_t aph = 0;
 #pragma unroll 1
-        while (i < nx) {
-            ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
-            if (!ok) break;
-            const uint64_t a = dw + off, b = dx + off;
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + 2 * k, b + 2 * k, idesc, !fresh(k));
-                tc_commit_addr(empty_s + 8u * (uint32_t)st);
+        for (int c0 = k0; c0 < k1; c0 += chunk_steps) {
+            if (c0 > k0) {
+                ok = wait_phase(smem_u32(acc_empty), aph, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                aph ^= 1;
             }
-            next_stage();
-        }
+            const int c1 = c0 + chunk_steps < k1 ? c0 + chunk_steps : k1;
+            const int nx = (c1 < L.xsteps ? c1 : L.xsteps) - c0;   // steps of x and W (<= 0: none)
+            i = 0;
 #pragma unroll 1
-        while (ok && i < n) {
-            ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
-            if (!ok) break;
-            const uint64_t a = db.base + off, b = dx + off;
-            if (elect_one()) {
+            while (i < nx) {
+                ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
+                if (!ok) break;
+                const uint64_t a = dw + off, b = dx + off;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + db.off[k], b + 2 * k, idesc, !fresh(k));
-                tc_commit_addr(empty_s + 8u * (uint32_t)st);
+                    for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + 2 * k, b + 2 * k, idesc, !fresh(k));
+                    tc_commit_addr(empty_s + 8u * (uint32_t)st);
+                }
+                next_stage();
             }
-            next_stage();
+#pragma unroll 1
+            while (ok && i < c1 - c0) {
+                ok = wait_phase(full_s + 8u * (uint32_t)st, ph, abort_flag);
+                if (!ok) break;
+                const uint64_t a = db.base + off, b = dx + off;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma_f16(acc_of(k), a + db.off[k], b + 2 * k, idesc, !fresh(k));
+                    tc_commit_addr(empty_s + 8u * (uint32_t)st);
+                }
+                next_stage();
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit(acc_full);
+            __syncwarp();
         }
-        if (ok && elect_one()) tc_commit(acc_full);
-        __syncwarp();
         if (!ok) fail();
     }
 
-    // ---- the CTA's partial tile into shared memory: part[token][128 rows]
+    // ---- the CTA's partial tile into shared memory: part[token][128 rows]; four
+    // warps take the first half of the tokens, four the second
     float* part = reinterpret_cast<float*>(ring);
-    if (warp < 4) {
-        if (wait_phase(smem_u32(acc_full), 0, abort_flag, 4 * kWaitClocks)) {
+    if (warp < 4 || warp >= 8) {
+        constexpr int kCols = TN / 2, kPiece = TN == 32 || TN == 64 ? 16 : 8;
+        const int half = warp < 4 ? 0 : kCols;
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)half;
+        float sum[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+        bool ok = true;
+        uint32_t aph = 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += chunk_steps) {
+            ok = wait_phase(smem_u32(acc_full), aph, abort_flag, 4 * kWaitClocks);
+            if (!ok) break;
+            aph ^= 1;
             tc_fence_after();
-            const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
-            constexpr int kCols = TN < 32 ? 16 : 32;
+            const int len = c0 + chunk_steps < n ? chunk_steps : n - c0;
+            const int naccs = 4 * len < C::kAccs ? 4 * len : C::kAccs;
 #pragma unroll 1
-            for (int c0 = 0; c0 < TN; c0 += kCols) {
-                float v[32];
-                if constexpr (TN == 16) {
-                    // two accumulators at a time: 32 columns
-                    float s16[16];
+            for (int a = 0; a < naccs; ++a) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s16[i] = 0.f;
-#pragma unroll 1
-                    for (int a = 0; a < naccs; a += 2) {
-                        tmem_ld32(t_lane + (uint32_t)(a * 16), v);
-                        tmem_wait_ld();
+                for (int c = 0; c < kCols; c += kPiece) {
+                    float v[kPiece];
+                    if constexpr (kPiece == 16) tmem_ld16(t_lane + (uint32_t)(a * TN + c), v);
+                    else tmem_ld8(t_lane + (uint32_t)(a * TN + c), v);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) s16[i] += v[i];
-                        if (a + 1 < naccs) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) s16[i] += v[16 + i];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) part[i * 128 + warp * 32 + lane] = s16[i];
-                } else {
-                    float sum[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[i] = 0.f;
-#pragma unroll 1
-                    for (int a = 0; a < naccs; ++a) {
-                        tmem_ld32(t_lane + (uint32_t)(a * TN + c0), v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[i] += v[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) part[(c0 + i) * 128 + warp * 32 + lane] = sum[i];
+                    for (int i = 0; i < kPiece; ++i) sum[c + i] += v[i];
                 }
             }
+            if (c0 + chunk_steps < n) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty);
+            }
+        }
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) part[(half + i) * 128 + (warp & 3) * 32 + lane] = sum[i];
             tc_fence_before();
         } else {
             fail();
