@@ -18,7 +18,7 @@
 // proportion).  For fp32 outputs (and V of two terms) the accumulators are
 // emptied and started again after at most kFinePieces pieces each: 7e-7 of the
 // result instead of 6e-6 at T = 128, 11008 -> 11008, for 23.2 instead of 22.2 us
-// at T = 64, 4096 -> 11008.  A bf16 output does not see the difference.
+// at T = 61, 11008 -> 4096.  A bf16 output does not see the difference.
 //
 // Routed products append the adapters to the contraction: after the columns of
 // x come those of V [T, E * rp] (every token's gated x A^T, zero for experts it

@@ -180,38 +180,51 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
     }
 }
 
-// The same decision in 32 bits for a warp's four tokens, eight lanes a token:
-// lane `sub` holds the logits of experts sub * EPL ..  Every value that a
-// comparison depends on carries a bound of its error, from the logits' (delta)
-// and from its own arithmetic.  Returns the experts whose logits have to be
-// known better before the decision stands (0: it stands, and the record is
-// written).  ends: 4 * EMAX floats of shared memory per token.  All lanes of
-// the warp call it; `valid` marks tokens that exist.
-template <int EPL>
+// The same decision in 32 bits, LPT lanes a token and EPL <= 2 experts a lane:
+// lane `sub` of the token holds the logits of experts sub + LPT * i.  Every value
+// that a comparison depends on carries a bound of its error, from the logits'
+// (delta) and from its own arithmetic.  Returns the experts whose logits have to
+// be known better before the decision stands (0: it stands, and the record is
+// written).  seg0: the token's first lane; ends: 4 * LPT * EPL floats of shared
+// memory per token.  All lanes of the warp call it; `valid` marks tokens that
+// exist.  What it costs is fetching its code, which every CTA runs once or a few
+// times: eight experts a lane, unrolled, took 30 us longer at E = 64.
+template <int LPT, int EPL>
 __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float delta, const GateParams& g, int sub,
-                                               bool valid, float* ends, int32_t* __restrict__ route,
-                                               int64_t t) {
+                                                   int seg0, bool valid, float* ends,
+                                                   int32_t* __restrict__ route, int64_t t) {
     constexpr uint32_t kAll = 0xffffffffu;
+    constexpr uint32_t kSeg = LPT == 32 ? kAll : (1u << LPT) - 1;
     auto seg_max = [](float v) {
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+        for (int off = LPT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
         return v;
     };
     auto seg_sum = [](float v) {
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+        for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
         return v;
     };
-    const int e0 = sub * EPL;
+    // one bit for every lane of the token, and for every expert
+    auto seg_bits = [&](bool p) { return __ballot_sync(kAll, p) >> seg0 & kSeg; };
+    auto expert_bits = [&](const bool (&p)[EPL]) {
+        uint64_t m = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m |= (uint64_t)seg_bits(p[i]) << (LPT * i);
+        return m;
+    };
     bool all = !(delta < 0.25f);   // every expert is open
-    uint32_t open = 0;             // open experts of this lane
+    bool in[EPL], on[EPL], open[EPL];
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        if (e0 + i < g.E) {
+    for (int i = 0; i < EPL; ++i) {
+        in[i] = sub + LPT * i < g.E;
+        open[i] = false;
+        if (in[i]) {
             all = all || !(fabsf(z[i]) <= 1e30f);   // infinities, NaN, near overflow
             m = fmaxf(m, z[i]);
         }
+    }
     m = seg_max(m);
     const float grow = delta * (1.f + 4.f * delta);   // e^(2 delta) - 1 over 2, bounded
     float s[EPL], q[EPL], eq[EPL];
@@ -223,7 +236,7 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
     for (int i = 0; i < EPL; ++i) {
         s[i] = 0.f;
         eq[i] = 0.f;
-        if (e0 + i < g.E) {
+        if (in[i]) {
             if (g.score == ADAFUSE_SCORE_SOFTMAX) {
                 s[i] = expf(z[i] - m);
                 eq[i] = 2.f * grow + 2e-6f + 1.2e-7f * (m - z[i]);
@@ -243,13 +256,13 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
             eq[i] *= s[i];
         }
     }
-    uint32_t on = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         q[i] = s[i];
-        if (e0 + i < g.E) {
-            const float b = g.bias != nullptr ? __ldg(g.bias + e0 + i) : 0.f;
-            if (b > -INFINITY) on |= 1u << i;
+        on[i] = false;
+        if (in[i]) {
+            const float b = g.bias != nullptr ? __ldg(g.bias + sub + LPT * i) : 0.f;
+            on[i] = b > -INFINITY;
             if (g.bias != nullptr) {
                 q[i] = s[i] + b;
                 eq[i] = isinf(b) ? 0.f : eq[i] + 1.2e-7f * fabsf(q[i]);
@@ -257,24 +270,35 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
         }
         eq[i] += 1e-37f;
     }
+    // what picks are ordered by, and how far off it may be
+    float key[EPL], ekey[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        key[i] = g.bias != nullptr ? q[i] : z[i];
+        ekey[i] = g.bias != nullptr ? eq[i] : delta;
+    }
     if (g.n_groups > 1) {
         // a group's worth lies between the sums of its best values' lower and
         // upper ends
         const int per = g.E / g.n_groups;
-        float *lo = ends, *hi = ends + 8 * EPL, *glo = hi + 8 * EPL, *ghi = glo + 8 * EPL;
+        float *lo = ends, *hi = ends + LPT * EPL, *glo = hi + LPT * EPL, *ghi = glo + LPT * EPL;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (e0 + i < g.E) {
-                lo[e0 + i] = on >> i & 1 ? q[i] - eq[i] : -INFINITY;
-                hi[e0 + i] = on >> i & 1 ? q[i] + eq[i] : -INFINITY;
+            if (in[i]) {
+                lo[sub + LPT * i] = on[i] ? q[i] - eq[i] : -INFINITY;
+                hi[sub + LPT * i] = on[i] ? q[i] + eq[i] : -INFINITY;
             }
         __syncwarp();
-        for (int grp = sub; grp < g.n_groups; grp += 8) {
+#pragma unroll 1
+        for (int grp = sub; grp < g.n_groups; grp += LPT) {
             float a = -INFINITY, b = -INFINITY, c = -INFINITY, d = -INFINITY;
+#pragma unroll 1
             for (int i = grp * per; i < (grp + 1) * per; ++i) {
                 const float v = lo[i], w = hi[i];
-                if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
-                if (w > c) { d = c; c = w; } else if (w > d) { d = w; }
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+                d = fmaxf(d, fminf(c, w));
+                c = fmaxf(c, w);
             }
             float wl = g.group_top == 2 && b > -INFINITY ? a + b : a;
             float wh = g.group_top == 2 && d > -INFINITY ? c + d : c;
@@ -286,61 +310,60 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
         __syncwarp();
         // a group is kept if fewer than top_groups may come before it, dropped
         // if at least that many must; anything else is open
-        unsigned long long keep = 0, unsure = 0;
-        for (int grp = sub; grp < g.n_groups; grp += 8) {
-            const float wl = glo[grp], wh = ghi[grp];
-            int may = 0, must = 0;
-            for (int i = 0; i < g.n_groups; ++i) {
-                if (i == grp) continue;
-                // a group with nothing enabled is worth -inf exactly
-                may += ghi[i] >= wl && (ghi[i] > -INFINITY || i < grp);
-                must += glo[i] > wh || (glo[i] == -INFINITY && wh == -INFINITY && i < grp);
-            }
-            if (may < g.top_groups) keep |= 1ull << grp;
-            else if (must < g.top_groups) unsure |= 1ull << grp;
-        }
+        bool keep[EPL], unsure[EPL];
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) {
-            keep |= __shfl_xor_sync(kAll, keep, off);
-            unsure |= __shfl_xor_sync(kAll, unsure, off);
+        for (int i = 0; i < EPL; ++i) {
+            const int grp = sub + LPT * i;
+            int may = 0, must = 0;
+            if (grp < g.n_groups) {
+                const float wl = glo[grp], wh = ghi[grp];
+#pragma unroll 1
+                for (int u = 0; u < g.n_groups; ++u) {
+                    // a group with nothing enabled is worth -inf exactly
+                    const float ul = glo[u], uh = ghi[u];
+                    may += u != grp && uh >= wl && (uh > -INFINITY || u < grp);
+                    must += u != grp && (ul > wh || (ul == -INFINITY && wh == -INFINITY && u < grp));
+                }
+            }
+            keep[i] = grp < g.n_groups && may < g.top_groups;
+            unsure[i] = grp < g.n_groups && !keep[i] && must < g.top_groups;
         }
+        const uint64_t kept = expert_bits(keep), doubt = expert_bits(unsure);
         // of an unsure group, the experts that may be among its best are open
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            if (e0 + i >= g.E) continue;
-            const int grp = (e0 + i) / per;
-            if (unsure >> grp & 1) {
-                if (on >> i & 1) {
-                    int above = 0;   // experts of the group surely before this one
-                    for (int u = grp * per; u < (grp + 1) * per; ++u) above += lo[u] > q[i] + eq[i];
-                    if (above < g.group_top) open |= 1u << i;
-                }
-            } else if (!(keep >> grp & 1)) {
-                on &= ~(1u << i);
+            if (!in[i]) continue;
+            const int grp = (sub + LPT * i) / per;
+            if (doubt >> grp & 1) {
+                int above = 0;   // experts of the group surely before this one
+#pragma unroll 1
+                for (int u = grp * per; u < (grp + 1) * per; ++u) above += lo[u] > q[i] + eq[i];
+                open[i] = on[i] && above < g.group_top;
+            } else if (!(kept >> grp & 1)) {
+                on[i] = false;
             }
         }
-        if (__any_sync(kAll, unsure != 0)) {
+        if (__any_sync(kAll, doubt != 0)) {
             // which experts the picks choose from depends on the groups: any
             // two of the kept and unsure groups' that are too close are open
+            const uint64_t cand = expert_bits(on);
             __syncwarp();
-            unsigned long long cand = (unsigned long long)on << e0;
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) cand |= __shfl_xor_sync(kAll, cand, off);
-            if (g.bias == nullptr) {
+            for (int i = 0; i < EPL; ++i)
+                if (in[i]) {
+                    lo[sub + LPT * i] = key[i] - ekey[i];
+                    hi[sub + LPT * i] = key[i] + ekey[i];
+                }
+            __syncwarp();
+            uint64_t rest = doubt != 0 ? cand : 0;
+#pragma unroll 1
+            while (rest != 0) {
+                const int u = __ffsll((long long)rest) - 1;
+                rest &= rest - 1;
+                const float l = lo[u], h = hi[u];
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (e0 + i < g.E) { lo[e0 + i] = z[i] - delta; hi[e0 + i] = z[i] + delta; }
-            }
-            __syncwarp();
-            if (unsure != 0) {
-#pragma unroll 1
-                for (int u = 0; u < g.E; ++u) {
-                    if (!(cand >> u & 1)) continue;
-                    const float l = lo[u], h = hi[u];
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        if ((on >> i & 1) && u != e0 + i && lo[e0 + i] <= h && l <= hi[e0 + i]) open |= 1u << i;
-                }
+                    if (on[i] && u != sub + LPT * i && key[i] - ekey[i] <= h && l <= key[i] + ekey[i]) open[i] = true;
             }
         }
         __syncwarp();
@@ -349,45 +372,39 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
     // ones apart); lane `sub` keeps pick number sub
     int my_pick = -1, n = 0;
     float my_z = 0.f, my_s = 0.f, zmax = -INFINITY;
+#pragma unroll 1
     for (int j = 0; j < g.k; ++j) {
-        int best = kMaxExperts;
-        float kb = 0.f, zb = 0.f, sb = 0.f, eb = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float key = g.bias != nullptr ? q[i] : z[i];
-            if ((on >> i & 1) && (best == kMaxExperts || key > kb)) {
-                best = e0 + i;
-                kb = key;
-                zb = z[i];
-                sb = s[i];
-                eb = g.bias != nullptr ? eq[i] : delta;
-            }
-        }
-#pragma unroll
-        for (int off = 4; off > 0; off >>= 1) {
-            const int ob = __shfl_xor_sync(kAll, best, off);
-            const float ok = __shfl_xor_sync(kAll, kb, off), oz = __shfl_xor_sync(kAll, zb, off);
-            const float os = __shfl_xor_sync(kAll, sb, off), oe = __shfl_xor_sync(kAll, eb, off);
-            if (ob < kMaxExperts && (best == kMaxExperts || ok > kb || (ok == kb && ob < best))) {
-                best = ob;
-                kb = ok;
-                zb = oz;
-                sb = os;
-                eb = oe;
-            }
-        }
-        const uint32_t mine = best / EPL == sub ? 1u << (best % EPL) : 0u;
-        on &= ~mine;
-        // who among the rest may really come before this pick
-        uint32_t rivals = 0;
+        float kb = -INFINITY;   // no enabled key is this low
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if ((on >> i & 1) && (g.bias != nullptr ? q[i] + eq[i] : z[i] + delta) >= kb - eb) rivals |= 1u << i;
-        // equal keys that are exact are settled by the index
-        if (best == kMaxExperts || isinf(kb) || (g.bias == nullptr && delta == 0.f)) rivals = 0;
-        open |= rivals;
-        if (__ballot_sync(kAll, rivals != 0) >> (threadIdx.x & 24) & 0xffu) open |= mine;
-        if (best < kMaxExperts) {
+            if (on[i]) kb = fmaxf(kb, key[i]);
+        kb = seg_max(kb);
+        bool hit[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) hit[i] = on[i] && key[i] == kb;
+        const uint64_t hits = expert_bits(hit);
+        const int best = hits != 0 ? __ffsll((long long)hits) - 1 : -1;
+        const int src = seg0 + (best >= 0 ? best % LPT : 0);
+        const bool second = EPL == 2 && best >= LPT;
+        const float zb = __shfl_sync(kAll, second ? z[EPL - 1] : z[0], src);
+        const float sb = __shfl_sync(kAll, second ? s[EPL - 1] : s[0], src);
+        const float eb = __shfl_sync(kAll, second ? ekey[EPL - 1] : ekey[0], src);
+        // who among the rest may really come before this pick; equal keys that
+        // are exact are settled by the index
+        const bool settled = best < 0 || isinf(kb) || (g.bias == nullptr && delta == 0.f);
+        bool rivals = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            if (best == sub + LPT * i) on[i] = false;
+            const bool rival = !settled && on[i] && key[i] + ekey[i] >= kb - eb;
+            open[i] = open[i] || rival;
+            rivals = rivals || rival;
+        }
+        const bool disputed = seg_bits(rivals) != 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (disputed && best == sub + LPT * i) open[i] = true;
+        if (best >= 0) {
             if (sub == j) { my_pick = best; my_z = zb; my_s = sb; }
             zmax = fmaxf(zmax, zb);
             n = j + 1;
@@ -401,12 +418,10 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
                 : expf(fminf(my_z, 0.f) - fminf(zmax, 0.f)) / (1.f + expf(-fabsf(my_z)));
     const float sum = seg_sum(x);
     if (g.renorm && n > 0) gate = x / sum;
+    uint64_t mask = expert_bits(open);
     // a score with a bias depends on every logit: known better all at once
-    if (open != 0 && g.bias != nullptr && g.score == ADAFUSE_SCORE_SOFTMAX) all = true;
-    unsigned long long mask = (unsigned long long)open << e0;
-    if (all) mask = g.E == 64 ? ~0ull : (1ull << g.E) - 1;
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) mask |= __shfl_xor_sync(kAll, mask, off);
+    if (mask != 0 && g.bias != nullptr && g.score == ADAFUSE_SCORE_SOFTMAX) all = true;
+    if (seg_bits(all) != 0) mask = g.E == 64 ? ~0ull : (1ull << g.E) - 1;
     if (valid && mask == 0 && sub < g.slots) {
         int32_t* rec = route + t * 2 * g.slots;
         rec[sub] = sub < n ? my_pick : -1;
@@ -434,11 +449,16 @@ template <typename H>
 __host__ __device__ constexpr uint32_t route_stage_bytes(int E) {
     return kRouteTokens * route_h_pitch<H>() + (uint32_t)kRouteDepth * route_w_pitch(E) * 4u + 256u;
 }
+// lanes that decide on a token, and the floats of shared memory they need
+template <int EMAX>
+__host__ __device__ constexpr int route_lanes() { return EMAX < 32 ? EMAX : 32; }
+template <int EMAX>
+__host__ __device__ constexpr int route_ends() { return kRouteThreads / route_lanes<EMAX>() * 4 * EMAX; }
 // after the loop: warps' partial logits and squares, the CTA's sums, the
 // groups' scratch, the logits in 64 bits; the fp64 pass reuses the start
 template <int EMAX>
 __host__ __device__ constexpr uint32_t route_tail_bytes() {
-    return 4u * ((kRouteWarps + 1) * (kRouteTokens + 1) * (EMAX + 1) + 4 * kRouteTokens * EMAX) + 64u +
+    return 4u * ((kRouteWarps + 1) * (kRouteTokens + 1) * (EMAX + 1) + route_ends<EMAX>()) + 64u +
            8u * (kRouteTokens + kRouteWarps) * kMaxExperts;
 }
 
@@ -676,10 +696,10 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     constexpr int kRow = EMAX + 1, kPart = (kRouteTokens + 1) * kRow;
     float* part = reinterpret_cast<float*>(smem);
     float* total = part + kRouteWarps * kPart;
-    float* ends = total + kPart;             // [32][4][EMAX], the groups' scratch
+    float* ends = total + kPart;             // the groups' scratch
     // the logits in 64 bits [32][64], then the fp64 pass's sums and scratch
     double* fixed = reinterpret_cast<double*>(
-        smem + ((4u * ((kRouteWarps + 1) * kPart + 4 * kRouteTokens * EMAX) + 15u) & ~15u));
+        smem + ((4u * ((kRouteWarps + 1) * kPart + route_ends<EMAX>()) + 15u) & ~15u));
     {
         float* mine = part + warp * kPart;
 #pragma unroll
@@ -741,41 +761,46 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     }
     const float* squares = zt + kRouteTokens / C * kRow;
 
-    // ---- decisions: CTA q takes tokens q, q + C, ...; eight lanes a token
-    constexpr int EPL = EMAX / 8;
+    // ---- decisions: CTA q takes tokens q, q + C, ...
+    constexpr int LPT = route_lanes<EMAX>(), EPL = EMAX / LPT;
     __shared__ uint64_t open_s[kRouteTokens];
-    const int sub = lane & 7;
-    const int t = q + C * (int)(threadIdx.x >> 3);
+    const int sub = lane % LPT, slot = (int)threadIdx.x / LPT;
     float wmax = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        if (sub * EPL + i < g.E) wmax = fmaxf(wmax, squares[sub * EPL + i]);
+        if (sub + LPT * i < g.E) wmax = fmaxf(wmax, squares[sub + LPT * i]);
 #pragma unroll
-    for (int off = 4; off > 0; off >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
-    const bool valid = t < ntok;
-    const float* zrow = zt + (valid ? t / C : 0) * kRow;
-    float z[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) z[i] = sub * EPL + i < g.E ? zrow[sub * EPL + i] : 0.f;
-    // 1.02: the squares are fp32 sums themselves; terms below fp32's normal
-    // range are off by up to 2^-149 each instead.  (A NaN in Wr shows in z.)
+    for (int off = LPT / 2; off > 0; off >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
     const int mine_chunks = (chunks + C - 1) / C;
     const float roundings = 49.f + kRouteRun + (float)(mine_chunks / kRouteRun) + (float)C;
-    // A router of zeros (as they are initialised) is exact.
-    const float delta = wmax == 0.f ? 0.f
-                                    : 1.02f * roundings * 0x1p-24f * sqrtf(zrow[EMAX]) * sqrtf(wmax) +
-                                          (float)d * 0x1p-148f;
-    const uint64_t open = route_decide32<EPL>(z, delta, g, sub, valid,
-                                              ends + (threadIdx.x >> 3) * 4 * EMAX, route, tok0 + t);
-    if (valid) {
-        if (sub == 0) open_s[t] = open;
-        if (open != 0) {
+    bool some_open = false;
+#pragma unroll 1
+    for (int r = slot; r - slot < kRouteTokens / C; r += kRouteThreads / LPT) {
+        const int t = q + C * r;
+        const bool valid = r < kRouteTokens / C && t < ntok;
+        const float* zrow = zt + (valid ? r : 0) * kRow;
+        float z[EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (sub * EPL + i < g.E) fixed[t * kMaxExperts + sub * EPL + i] = (double)z[i];
+        for (int i = 0; i < EPL; ++i) z[i] = sub + LPT * i < g.E ? zrow[sub + LPT * i] : 0.f;
+        // 1.02: the squares are fp32 sums themselves; terms below fp32's normal
+        // range are off by up to 2^-149 each instead.  (A NaN in Wr shows in z.)
+        // A router of zeros (as they are initialised) is exact.
+        const float delta = wmax == 0.f ? 0.f
+                                        : 1.02f * roundings * 0x1p-24f * sqrtf(zrow[EMAX]) * sqrtf(wmax) +
+                                              (float)d * 0x1p-148f;
+        const uint64_t open = route_decide32<LPT, EPL>(z, delta, g, sub, lane - sub, valid, ends + slot * 4 * EMAX,
+                                                       route, tok0 + t);
+        if (valid) {
+            if (sub == 0) open_s[t] = open;
+            if (open != 0) {
+                some_open = true;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (sub + LPT * i < g.E) fixed[t * kMaxExperts + sub + LPT * i] = (double)z[i];
+            }
         }
     }
-    if (!__syncthreads_or(valid && open != 0)) return;
+    if (!__syncthreads_or(some_open)) return;
 
     // ---- what the bounds left open, in fp64: for each token the CTA sums two
     // open logits at a time (most often there are two), a thread every 256th
