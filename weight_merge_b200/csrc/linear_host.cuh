@@ -95,7 +95,10 @@ inline RoutedLayout routed_layout(const adafuse_ctx* ctx, const PairDesc& pd, in
 
 // A launch on clusters that may be set up while the launch before it ends:
 // every kernel launched here executes griddepcontrol.wait before it touches
-// memory an earlier launch may write (or relies on one that did).
+// memory an earlier launch may write (or relies on one that did), and lets the
+// launch after it be set up once all its own CTAs run (1 to 2 us a call where
+// calls follow each other).  A launch is complete only after what it waited for,
+// so waiting for the one before is waiting for all.
 template <typename Kernel, typename... Args>
 cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s,
                             const Args&... args) {

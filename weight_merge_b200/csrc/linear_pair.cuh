@@ -109,7 +109,7 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (MODE == kDown || L.vsteps == 0) pdl_wait();   // as in the skinny kernel
-    if (MODE == kDown) pdl_launch_dependents();
+    pdl_launch_dependents();
     const uint32_t peer_abort = cluster_addr((const void*)abort_flag, q ^ 1u);
     auto fail = [&]() {
         if (!*abort_flag) {

@@ -347,7 +347,7 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     // product goes on: its x, W and B were complete before the kDown launch let
     // it start, and only V is waited for.
     if (MODE == kDown || L.vsteps == 0) pdl_wait();
-    if (MODE == kDown) pdl_launch_dependents();
+    pdl_launch_dependents();
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(L.p.status, ADAFUSE_STATUS_TIMEOUT);

@@ -134,8 +134,8 @@ linear_stream_kernel(const LinearParams p, const uint16_t* __restrict__ W, const
     // A routed product starts while the kDown launch before it runs: its x and W
     // were complete before that launch let it start, and u is waited for below.
     if constexpr (MODE != kRouted) pdl_wait();
+    pdl_launch_dependents();
     if constexpr (MODE == kDown) {
-        pdl_launch_dependents();
         // experts that some token chose; a unit of rows none of them owns is
         // neither read nor written
         if (threadIdx.x == 0) used_s = 0;

@@ -633,6 +633,7 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     int in_run = 0;
 
     sm100::pdl_wait();   // set-up overlaps the end of the launch before this one
+    sm100::pdl_launch_dependents();
 #pragma unroll
     for (int s = 0; s < kRouteStages - 1; ++s) load_chunk(q + s * C, s);
     int stage = 0;
