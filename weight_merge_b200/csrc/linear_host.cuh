@@ -150,6 +150,7 @@ cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMa
                            map_x, map_b, map_v, S, stages);
 }
 
+// The smallest tile that holds the tokens, up to 128.
 template <int MODE>
 cudaError_t launch_skinny_any(const TcLinear& L, const CUtensorMap& map_w, const CUtensorMap& map_b,
                               const adafuse_ctx* ctx, cudaStream_t s) {

@@ -32,11 +32,12 @@ using sm100::pdl_wait;
 constexpr int kStreamWarps = 16;
 constexpr int kStreamThreads = 32 * kStreamWarps;
 constexpr int kStreamRows = 16;
+// As many tokens as an MMA has columns.  4096 -> 11008: T = 1 15.9 us, T = 8 18.7;
+// on the tensor-core kernel for more tokens 20.0 and 19.5.
 constexpr int kStreamMaxTokens = 8;
-#ifndef SDEPTH
-#define SDEPTH 2
-#endif
-constexpr int kStreamDepth = SDEPTH;   // steps in flight per warp, 2 KB each
+// Steps in flight per warp, 2 KB each (T = 1, 4096 -> 11008: 16.8, 16.2 and 24.8 us
+// for one, two and three, which spill).
+constexpr int kStreamDepth = 2;
 
 // 16 consecutive bf16 of a row (n = 16, 8 or 0 of them inside it), read past L1.
 // WIDE: p is 32-byte aligned and n is 16 or 0.
