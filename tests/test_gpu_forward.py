@@ -740,6 +740,53 @@ def test_two_graphs_at_once(T):
     assert sw.status(stream()) == 0
 
 
+@pytest.mark.parametrize("T", [2, 8, 30, 200])
+def test_chain_of_calls_over_one_buffer(T):
+    """Calls that follow each other without a gap, each reading what the one
+    before wrote in place: residual and factor, then x, then the router's rows."""
+    n, E, r = 264, 8, 4
+    m, sw = model(n, n, E=E, r=r, seed=T)
+    g = gen(T)
+    Wr = torch.randn((n, E), generator=g, device="cuda") * 0.05
+    x, rt = rows(g, T, n), make_routes(g, T, E, 2, 2)
+    ws = workspace(sw, T, False)
+    first = rows(g, T, n).contiguous()
+    steps = 12
+    hist = [[torch.empty_like(first) for _ in range(2)] for _ in range(steps)]
+    recs = torch.zeros((steps, T, 4), dtype=torch.int32, device="cuda")
+    a, b = first.clone(), first.clone()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        s = torch.cuda.current_stream().cuda_stream
+        for i in range(steps):
+            sw.linear(0, 0, x, a, residual=a, stream=s)                     # a <- a + x W
+            hist[i][0].copy_(a)
+            sw.linear_routed(0, 0, a, rt, b, ws, residual=b, stream=s)      # b <- b + a W'
+            sw.route_experts(b, Wr, Bnd.make_gating(k=2), recs[i], s)
+            hist[i][1].copy_(b)
+            sw.linear(0, 0, b, a, activation=ACT["relu"], mul=a, stream=s)  # a <- a relu(b W)
+            sw.linear_routed(0, 0, x, recs[i], a, ws, stream=s)             # a <- x W''
+    for _ in range(2):
+        a.copy_(first)
+        b.copy_(first)
+        graph.replay()
+        torch.cuda.synchronize()
+    pa, pb = first, first
+    kw = dict(slots=2, A=m.A[0], B=m.B[0], s=2.0)
+    for i in range(steps):
+        check(hist[i][0], *ref.product(x, m.W[0], residual=pa))
+        check(hist[i][1], *ref.product(hist[i][0], m.W[0], residual=pb, routes=rt, **kw))
+        pb = hist[i][1]
+        idx, _, _ = ref.route(pb, Wr, score="softmax", k=2)
+        assert np.array_equal(recs[i, :, :2].cpu().numpy(), idx)
+        pa = torch.empty_like(first)
+        sw.linear_routed(0, 0, x, recs[i], pa, ws, stream=stream())
+        torch.cuda.synchronize()
+        check(pa, *ref.product(x, m.W[0], routes=recs[i], **kw))
+    check(a, *ref.product(x, m.W[0], routes=recs[-1], **kw))
+
+
 def test_linear_refusals():
     import ctypes
     inn, out, T = 64, 72, 4

@@ -229,16 +229,15 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     L.terms = lay.terms;
     L.b_swizzled = lay.rp == 16 || lay.rp == 32 || lay.rp == 64;
     L.v = static_cast<uint16_t*>(workspace);
+    cudaError_t e = cudaSuccess;
     if (lay.pad) {
         uint16_t* padded = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + lay.v_bytes);
         const int64_t nrows = (int64_t)p.E * p.out;
-        const unsigned grid =
-            (unsigned)std::min<int64_t>(ceil_div(nrows * lay.rp, 256), (int64_t)ctx->sm_count * 8);
-        pad_b_kernel<<<grid, 256, 0, s>>>(p.B, padded, nrows, p.r, lay.rp);
+        const int64_t grid = std::min<int64_t>(ceil_div(nrows * lay.rp, 256), (int64_t)ctx->sm_count * 8);
+        e = launch_clusters(pad_b_kernel, grid, 256, 0, 1, s, p.B, padded, nrows, p.r, lay.rp);
         p.B = padded;
     }
     L.bsteps = (int)ceil_div((int64_t)p.E * lay.rp, 64);
-    cudaError_t e = cudaGetLastError();
     for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
         L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
         L.vsteps = 0;

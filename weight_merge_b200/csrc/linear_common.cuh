@@ -275,8 +275,8 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, int64_t tok0
 __device__ __forceinline__ bool route_slot(const int32_t* routes, int slots, int E, int64_t t, int j,
                                            int& e, float& gate, int& bad) {
     const int32_t* rec = routes + t * 2 * slots;
-    e = __ldg(rec + j);
-    gate = __int_as_float(__ldg(rec + slots + j));
+    e = rec[j];
+    gate = __int_as_float(rec[slots + j]);
     if (e == -1) return false;
     if (e < -1 || e >= E) { bad |= ADAFUSE_STATUS_BAD_EXPERT; return false; }
     if (!isfinite(gate)) { bad |= ADAFUSE_STATUS_BAD_GATE; return false; }

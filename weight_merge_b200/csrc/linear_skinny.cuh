@@ -556,6 +556,8 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
 __global__ void __launch_bounds__(256)
 pad_b_kernel(const uint16_t* __restrict__ B, uint16_t* __restrict__ dst, int64_t nrows, int r, int rp) {
     const int64_t total = nrows * rp;
+    pdl_wait();   // the launch before may still read dst
+    pdl_launch_dependents();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / rp;
         const int k = (int)(i % rp);

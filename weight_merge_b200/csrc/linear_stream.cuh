@@ -9,7 +9,9 @@
 // sides, those and the same columns of one token's x are the A and B fragments
 // of four mma.m16n8k16 as they stand, so W goes from memory through registers
 // to the tensor cores.  A warp's next kStreamDepth steps, the next unit's
-// included, are requested as soon as the last ones are consumed.  x stays in L1.
+// included, are requested as soon as the last ones are consumed.  x stays in L1
+// (plain loads: a launch set up while the one before it still writes must not read
+// its output as constant data).
 //
 // Every sum is fp32; the partial sums of the warps and of the cluster's CTAs
 // are added in a fixed order.
@@ -214,8 +216,8 @@ linear_stream_kernel(const LinearParams p, const uint16_t* __restrict__ W, const
 #pragma unroll
             for (int d = 0; d < kStreamDepth; ++d) {
                 const int k = k0 + d * step, n = p.in - c16 - k;
-                const uint4 x0 = tok && n > 0 ? __ldg(reinterpret_cast<const uint4*>(xt + k)) : zero;
-                const uint4 x1 = tok && n > 8 ? __ldg(reinterpret_cast<const uint4*>(xt + k + 8)) : zero;
+                const uint4 x0 = tok && n > 0 ? *reinterpret_cast<const uint4*>(xt + k) : zero;
+                const uint4 x1 = tok && n > 8 ? *reinterpret_cast<const uint4*>(xt + k + 8) : zero;
                 mma_bf16_16816(acc, a[d][0], b[d][0], a[d][1], b[d][1], x0.x, x0.y);
                 mma_bf16_16816(acc, a[d][2], b[d][2], a[d][3], b[d][3], x0.z, x0.w);
                 mma_bf16_16816(acc, a[d][4], b[d][4], a[d][5], b[d][5], x1.x, x1.y);

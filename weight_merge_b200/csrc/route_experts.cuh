@@ -529,9 +529,17 @@ __device__ __forceinline__ void route_h_frag(const __nv_bfloat16* r0, const __nv
         s = fmaf(x, x, fmaf(y, y, s));
     }
 }
-__device__ __forceinline__ float route_load(const float* p) { return __ldg(p); }
+// h may come from the launch before, under whose end this one is set up: it is
+// no constant data.
+__device__ __forceinline__ float route_load(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ float route_load(const __nv_bfloat16* p) {
-    return __bfloat162float(__ldg(p));
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return __uint_as_float((uint32_t)v << 16);
 }
 
 // h_piece / w_piece: bytes of a copy (16, or 8 / 4 where rows or Wr are aligned
