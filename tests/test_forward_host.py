@@ -28,6 +28,8 @@ def test_structs_have_the_c_layout():
     assert ctypes.sizeof(Bnd.Route8) == 64
     assert ctypes.sizeof(Bnd.Gating) == 40 and Bnd.Gating.bias.offset == 32
     assert ctypes.sizeof(Bnd.LinearArgs) == 104 and Bnd.LinearArgs.T.offset == 24
+    fields = (1, 2, 3, 4, 5, 2 ** 40, 2 ** 62 + 1, 7, 8, 9, 10, 11, 12, 13, 14)
+    assert Bnd._pack_linear_args(*fields) == bytes(Bnd.LinearArgs(*fields))
 
 
 def test_route_by_hand():

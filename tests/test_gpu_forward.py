@@ -307,6 +307,8 @@ def test_route_refusals():
         sw.route_experts(h, Wr[:, :4], Bnd.make_gating(), rt, stream())
     with pytest.raises(ValueError):
         sw.route_experts(h, Wr, Bnd.make_gating(bias=torch.zeros(4, device="cuda")), rt, stream())
+    with pytest.raises(ValueError):
+        Bnd.make_gating(bias=torch.zeros((2, 4), device="cuda"))
 
 
 # --------------------------------------------------------------------------
@@ -330,6 +332,24 @@ def test_linear_shapes(T, inn, out, dtype):
     assert (y[T] == 7).all()
     check(y[:T], *ref.product(x, m.W[0], out_dtype=dtype))
     assert sw.status(stream()) == 0
+
+
+@pytest.mark.parametrize("T", [2, 9, 40, 130, 300])
+@pytest.mark.parametrize("inn,out,E,r", [(8, 8, 1, 1), (8, 40, 5, 8), (24, 8, 2, 16), (56, 16, 64, 2), (72, 8, 3, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_smaller_than_any_tile(T, inn, out, E, r, dtype):
+    m, sw = model(out, inn, E=E, r=r, seed=T)
+    g = gen(T + inn)
+    x, rt = rows(g, T, inn, BF, pad=8), make_routes(g, T, E, min(E, 2), 2)
+    full = torch.full((T + 1, out + 8), 3.0, dtype=dtype, device="cuda")
+    y = full[:T, :out]
+    sw.linear(0, 0, x, y, stream=stream())
+    torch.cuda.synchronize()
+    check(y, *ref.product(x, m.W[0], out_dtype=dtype))
+    sw.linear_routed(0, 0, x, rt, y, workspace(sw, T, dtype == F32), stream=stream())
+    torch.cuda.synchronize()
+    check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0, out_dtype=dtype))
+    assert (full[:, out:] == 3).all() and (full[T] == 3).all()
 
 
 @pytest.mark.parametrize("T", [1, 6, 40, 150, 600])

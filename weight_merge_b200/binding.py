@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +88,11 @@ class LinearArgs(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
+# A LinearArgs as bytes (building the structure field by field takes five times
+# as long, and the calls for one token are bound by the host).
+_pack_linear_args = struct.Struct("<5i4x10q").pack
+
+
 class Target(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("out", ctypes.c_int64), ("in_", ctypes.c_int64),
                 ("W", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p)]
@@ -144,9 +150,9 @@ def lib() -> ctypes.CDLL:
         "adafuse_refresh_adapters": ([P, P], ctypes.c_int),
         "adafuse_route_experts": ([P, P, i32, i64, i64, i64, P, ctypes.POINTER(Gating), i32, P, P],
                                   ctypes.c_int),
-        "adafuse_linear": ([P, ctypes.POINTER(LinearArgs), P], ctypes.c_int),
+        "adafuse_linear": ([P, P, P], ctypes.c_int),
         "adafuse_linear_workspace": ([P, i32, i32, i64, i32, ctypes.POINTER(i64)], ctypes.c_int),
-        "adafuse_linear_routed": ([P, ctypes.POINTER(LinearArgs), P, i32, P, i64, P], ctypes.c_int),
+        "adafuse_linear_routed": ([P, P, P, i32, P, i64, P], ctypes.c_int),
         "adafuse_segment_table": ([ctypes.POINTER(Desc), P, i64, ctypes.POINTER(i64)], ctypes.c_int),
         "adafuse_tile_size": ([], ctypes.c_int),
         "adafuse_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -370,6 +376,8 @@ def make_gating(score: int = ADAFUSE_SCORE_SOFTMAX, k: int = 2, n_groups: int = 
     """bias: a device fp32 tensor of E values (kept alive by the returned struct) or None."""
     if bias is not None:
         _need(bias, "float32", "bias")
+        if bias.dim() != 1:
+            raise ValueError(f"bias: shape {tuple(bias.shape)}, expected one value per expert")
     g = Gating(int(score), int(k), int(n_groups), int(top_groups), int(group_top), int(renorm),
                float(scale), None if bias is None else bias.data_ptr())
     g._keep = bias
@@ -529,9 +537,9 @@ class Switcher:
         dev = self._device
         xp, ldx = _rows(x, self._bf16, T, inn, dev, "x")
         yp, ldy = _rows(y, dtype, T, out, dev, "y")
-        mp, ldm = (None, 0) if mul is None else _rows(mul, dtype, T, out, dev, "mul")
-        rp, ldr = (None, 0) if residual is None else _rows(residual, dtype, T, out, dev, "residual")
-        bp = None
+        mp, ldm = (0, 0) if mul is None else _rows(mul, dtype, T, out, dev, "mul")
+        rp, ldr = (0, 0) if residual is None else _rows(residual, dtype, T, out, dev, "residual")
+        bp = 0
         if bias is not None:
             if bias.shape != (out,):
                 raise ValueError(f"bias: shape {tuple(bias.shape)}, expected {(out,)}")
@@ -539,15 +547,15 @@ class Switcher:
             if bias.get_device() != dev:
                 raise ValueError(f"bias: on {bias.device}, the context is on cuda:{dev}")
             bp = bias.data_ptr()
-        return LinearArgs(layer, target, ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT,
-                          activation, io, T, xp, ldx, bp, mp, ldm, rp, ldr, yp, ldy)
+        return _pack_linear_args(layer, target, ADAFUSE_WEIGHT_BASE if base else ADAFUSE_WEIGHT_CURRENT,
+                                 activation, io, T, xp, ldx, bp, mp, ldm, rp, ldr, yp, ldy)
 
     def linear(self, layer: int, target: int, x, y, bias=None, activation: int = ADAFUSE_ACT_NONE,
                mul=None, residual=None, base: bool = False, stream: int = 0) -> None:
         """y = residual + mul * act(x W^T + bias) with W of (layer, target), or
         its registered pristine copy when ``base``."""
         a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
-        code = self._lib.adafuse_linear(self.ctx, ctypes.byref(a), stream or None)
+        code = self._lib.adafuse_linear(self.ctx, a, stream or None)
         if code:
             raise AdafuseError(code, "adafuse_linear")
 
@@ -564,12 +572,12 @@ class Switcher:
         linear_workspace() bytes that no overlapping call uses."""
         a = self._linear_args(layer, target, x, y, bias, activation, mul, residual, base)
         slots = routes.shape[-1] // 2
-        rp, ldr = _rows(routes, self._i32, a.T, 2 * slots, self._device, "routes")
+        rp, ldr = _rows(routes, self._i32, x.shape[0], 2 * slots, self._device, "routes")
         if ldr != 2 * slots:
             raise ValueError("routes: one contiguous record per row of x")
-        if workspace.get_device() != self._device:
-            raise ValueError(f"workspace: on {workspace.device}")
-        code = self._lib.adafuse_linear_routed(self.ctx, ctypes.byref(a), rp, slots,
+        if workspace.get_device() != self._device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: not contiguous memory on cuda:{self._device}")
+        code = self._lib.adafuse_linear_routed(self.ctx, a, rp, slots,
                                                workspace.data_ptr(), workspace.nbytes, stream or None)
         if code:
             raise AdafuseError(code, "adafuse_linear_routed")
