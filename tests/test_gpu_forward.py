@@ -435,6 +435,7 @@ ROUTED = [
     (65, 128, 200, 7, 20, 4, 4, 0.1), (128, 512, 512, 8, 8, 2, 2, 0.0), (200, 264, 136, 12, 40, 6, 8, 0.3),
     (257, 192, 1032, 4, 32, 3, 4, 0.0), (300, 512, 256, 16, 64, 2, 2, 0.1), (513, 72, 264, 9, 5, 2, 2, 0.0),
     (600, 320, 520, 64, 64, 8, 8, 0.0), (1025, 256, 384, 8, 8, 2, 2, 1.0),
+    (150, 2048, 1032, 8, 8, 2, 2, 0.0), (250, 2048, 1024, 8, 16, 2, 2, 0.1), (333, 2048, 4104, 4, 4, 3, 4, 0.1),
 ]
 
 

@@ -7,6 +7,8 @@
 
 #include <algorithm>
 #include <cstring>
+#include <mutex>
+#include <vector>
 
 #include "context.cuh"
 #include "linear_pair.cuh"
@@ -119,20 +121,62 @@ cudaError_t launch_clusters(Kernel kernel, int64_t grid, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Cluster size of the skinny kernel: the contraction is split while the grid
-// stays within one CTA an SM and every CTA keeps at least four steps.  Measured
-// at T = 61 (4096 -> 1024, 4096 -> 4096, 11008 -> 4096, 4096 -> 11008): 10.2,
-// 13.1, 21.6 and 21.5 us at the sizes this takes (8, 4, 4, 1: 10.5, 13.1, 21.6,
-// 21.5), up to twice that at the others.
-inline int skinny_split(int64_t tiles, int nsteps, int sm_count) {
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= sm_count && nsteps / (S * 2) >= 4) S *= 2;
-    return S;
+// Clusters of 2, 4 and 8 CTAs of the skinny kernel, one CTA an SM, that the device
+// runs at once: fewer than its SMs, since a cluster stays within one group of
+// them.  Asked once per device.
+struct ClusterRoom {
+    int device, of[4];   // of[i]: clusters of 1 << i
+};
+inline ClusterRoom cluster_room(const adafuse_ctx* ctx) {
+    static std::mutex mu;
+    static std::vector<ClusterRoom> known;
+    std::lock_guard<std::mutex> lk(mu);
+    for (const ClusterRoom& r : known)
+        if (r.device == ctx->device) return r;
+    using C = SkinnyConfig<128>;
+    auto kernel = linear_skinny_kernel<128, kProduct>;
+    ensure_smem_attr(kernel, C::smem_bytes(C::stages(1)), ctx->device);
+    ClusterRoom r = {ctx->device, {ctx->sm_count, 0, 0, 0}};
+    for (int i = 1; i < 4; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)ctx->sm_count >> i << i, 1, 1);
+        cfg.blockDim = dim3(kSkinnyThreads, 1, 1);
+        cfg.dynamicSmemBytes = C::smem_bytes(C::stages(1));
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&r.of[i], kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            r.of[i] = 0;   // the contraction is not split that far
+        }
+    }
+    try {
+        known.push_back(r);
+    } catch (...) {
+        // not remembered: asked again
+    }
+    return r;
+}
+
+// Cluster size of the skinny kernel: the contraction is split while all clusters
+// run at once, beside the `busy` CTAs of the launch before, and every CTA keeps
+// at least four steps.  Measured at T = 61 (4096 -> 1024, 4096 -> 4096, 11008 -> 4096,
+// 4096 -> 11008): 10.2, 13.1, 21.6 and 21.5 us at the sizes this takes (8, 4, 4, 1),
+// up to twice that at the others.  A cluster that
+// finds no room runs in a second wave: T = 250, 4096 -> 1024 with 8 experts of rank 16
+// took 34.9 us on clusters of 8 and 21.1 on clusters of 4.
+inline int skinny_split(int64_t tiles, int nsteps, int busy, const ClusterRoom& room) {
+    int i = 0;
+    while (i < 3 && tiles <= room.of[i + 1] - (busy >> (i + 1)) - (busy > 0) && nsteps >> (i + 1) >= 4) ++i;
+    return 1 << i;
 }
 
 template <int TN, int MODE>
 cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMap& map_b, const adafuse_ctx* ctx,
-                          cudaStream_t s) {
+                          cudaStream_t s, int* ctas) {
     using C = SkinnyConfig<TN>;
     CUtensorMap map_x, map_v;
     std::memset(&map_v, 0, sizeof map_v);
@@ -140,8 +184,9 @@ cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMa
     if (L.vsteps > 0 && !encode_v(&map_v, L, TN)) return cudaErrorInvalidValue;
     L.tok_tiles = (int)ceil_div(L.p.T, TN);
     const int64_t tiles = ceil_div(L.rows, L.tile_rows) * L.tok_tiles;
-    const int S = skinny_split(tiles, L.xsteps + L.vsteps, ctx->sm_count);
+    const int S = skinny_split(tiles, L.xsteps + L.vsteps, L.busy, cluster_room(ctx));
     if (tiles * S > INT32_MAX) return cudaErrorInvalidConfiguration;
+    *ctas = (int)(tiles * S);
     const int stages = C::stages(tiles * S <= ctx->sm_count ? 1 : 2);
     auto kernel = linear_skinny_kernel<TN, MODE>;
     ensure_smem_attr(kernel, C::smem_bytes(C::stages(1)), ctx->device);
@@ -152,12 +197,12 @@ cudaError_t launch_skinny(TcLinear L, const CUtensorMap& map_w, const CUtensorMa
 // The smallest tile that holds the tokens, up to 128.
 template <int MODE>
 cudaError_t launch_skinny_any(const TcLinear& L, const CUtensorMap& map_w, const CUtensorMap& map_b,
-                              const adafuse_ctx* ctx, cudaStream_t s) {
+                              const adafuse_ctx* ctx, cudaStream_t s, int* ctas) {
     const int64_t T = L.p.T;
-    if (T <= 16) return launch_skinny<16, MODE>(L, map_w, map_b, ctx, s);
-    if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, ctx, s);
-    if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, ctx, s);
-    return launch_skinny<128, MODE>(L, map_w, map_b, ctx, s);
+    if (T <= 16) return launch_skinny<16, MODE>(L, map_w, map_b, ctx, s, ctas);
+    if (T <= 32) return launch_skinny<32, MODE>(L, map_w, map_b, ctx, s, ctas);
+    if (T <= 64) return launch_skinny<64, MODE>(L, map_w, map_b, ctx, s, ctas);
+    return launch_skinny<128, MODE>(L, map_w, map_b, ctx, s, ctas);
 }
 
 // Grid of the stream kernel: two CTAs an SM less `reserve` CTAs, or, where
@@ -207,12 +252,12 @@ inline int pair_width(int64_t tok_tiles, int rows, int64_t pairs, int nsteps, do
 // split) where its estimate is below the pair kernel's, that is where the pair
 // kernel has too few tiles to occupy the SMs.  Measured at T = 333 4096 -> 1024:
 // 13.8 against 17.6 us; T = 1037 4096 -> 1024: 15.4 against 17.4 us.
-inline bool pair_is_faster(const TcLinear& L, int sm_count) {
-    const int nsteps = L.xsteps + L.vsteps;
+inline bool pair_is_faster(const TcLinear& L, const adafuse_ctx* ctx) {
+    const int nsteps = L.xsteps + L.vsteps, sm_count = ctx->sm_count;
     double pair_us;
-    pair_width(ceil_div(L.p.T, kPairTokens), L.rows, sm_count / 2, nsteps, &pair_us);
+    pair_width(ceil_div(L.p.T, kPairTokens), L.rows, (sm_count - L.busy) / 2, nsteps, &pair_us);
     const int64_t tiles = ceil_div(L.rows, L.tile_rows) * ceil_div(L.p.T, 128);
-    const int S = skinny_split(tiles, nsteps, sm_count);
+    const int S = skinny_split(tiles, nsteps, L.busy, cluster_room(ctx));
     const double skinny_us = 7.0 + (double)(ceil_div(tiles * S, sm_count) * ceil_div(nsteps, S)) * 0.19;
     return pair_us <= skinny_us;
 }
@@ -221,7 +266,7 @@ inline bool pair_is_faster(const TcLinear& L, int sm_count) {
 template <bool F32, int MODE>
 cudaError_t launch_pair(TcLinear L, const uint16_t* W, const adafuse_ctx* ctx, cudaStream_t s) {
     L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
-    const int64_t most = ctx->sm_count / 2;
+    const int64_t most = (ctx->sm_count - L.busy) / 2;
     double us;
     const int BN = pair_width(L.tok_tiles, L.rows, most, L.xsteps + L.vsteps, &us);
     CUtensorMap map_w, map_x, map_b, map_v;
@@ -244,28 +289,35 @@ inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream
     L.rows = L.p.out;
     L.tile_rows = 128;
     L.xsteps = (int)ceil_div(L.p.in, 64);
-    if (L.p.T > 128 && pair_is_faster(L, ctx->sm_count))
+    if (L.p.T > 128 && pair_is_faster(L, ctx))
         return L.p.f32 ? launch_pair<true, kProduct>(L, L.p.W, ctx, s) : launch_pair<false, kProduct>(L, L.p.W, ctx, s);
     CUtensorMap map_w, map_b;
     std::memset(&map_b, 0, sizeof map_b);
     if (!encode_rows(&map_w, L.p.W, L.p.out, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
     if (L.vsteps > 0 && !encode_b(&map_b, L, 128)) return cudaErrorInvalidValue;
-    return launch_skinny_any<kProduct>(L, map_w, map_b, ctx, s);
+    int ctas;
+    return launch_skinny_any<kProduct>(L, map_w, map_b, ctx, s, &ctas);
 }
 
-// V of a routed product.
-inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s) {
+// V of a routed product.  Returns in *busy the CTAs that the product launched
+// next leaves their SMs: this launch's where they are few, so that the product
+// runs beside them (where they are many, it starts as they end).
+inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s, int* busy) {
     CUtensorMap map_a, none;
     std::memset(&none, 0, sizeof none);
     L.rows = L.p.E * L.p.r;
     L.tile_rows = 128 / L.p.r * L.p.r;
     L.xsteps = (int)ceil_div(L.p.in, 64);
-    L.vsteps = 0;
-    if (L.p.T > 128 && L.rp == L.p.r && pair_is_faster(L, ctx->sm_count))
+    L.vsteps = L.busy = 0;
+    *busy = 0;
+    if (L.p.T > 128 && L.rp == L.p.r && pair_is_faster(L, ctx))
         return L.terms == 2 ? launch_pair<true, kDown>(L, L.p.A, ctx, s)
                             : launch_pair<false, kDown>(L, L.p.A, ctx, s);
     if (!encode_rows(&map_a, L.p.A, L.rows, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
-    return launch_skinny_any<kDown>(L, map_a, none, ctx, s);
+    int ctas = 0;
+    const cudaError_t e = launch_skinny_any<kDown>(L, map_a, none, ctx, s, &ctas);
+    if (ctas <= ctx->sm_count / 4) *busy = ctas;
+    return e;
 }
 
 }  // namespace adafuse

@@ -49,6 +49,7 @@ struct TcLinear {
     int rows;          // kDown: E * r; otherwise out
     int tile_rows;     // rows of a tile that are its own: 128, or whole experts of kDown
     int tok_tiles;     // token tiles
+    int busy;          // SMs that the launch before holds (host only)
 };
 
 constexpr int kSkinnyThreads = 384;
