@@ -439,7 +439,9 @@ constexpr int kRouteRun = 6;
 
 // Shared memory of a stage: h rows padded by 16 bytes, then rows of Wr padded to
 // 4 or 12 floats past a multiple of 16, so that fragment reads fall into
-// different banks; 256 bytes of slack for the reads past the last expert.
+// different banks (rows that no 16-byte copy divides are not padded: the chunk is
+// copied as it lies.  T = 2376 5072 x 62: 125 us, in copies of 4 bytes to padded rows
+// 219); 256 bytes of slack for the reads past the last expert.
 template <typename H>
 __host__ __device__ constexpr uint32_t route_h_pitch() { return kRouteDepth * (uint32_t)sizeof(H) + 16; }
 __host__ __device__ constexpr int route_w_pitch(int E) {   // in floats
@@ -570,9 +572,10 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     const H* hrow = h + (tok0 + (row_in ? row : 0)) * ldh;
     const uint32_t h_dst = smem_s + (uint32_t)row * kPitch;
     const uint32_t w_dst = smem_s + kRouteTokens * kPitch;
-    const int w_pitch = route_w_pitch(g.E);
+    const bool padded = w_piece == 16 && (g.E & 3) == 0;
+    const int w_pitch = padded ? route_w_pitch(g.E) : g.E;
+    const bool vec = h_piece == 16 && padded;
     const uint32_t w_row = (uint32_t)w_pitch * 4u;
-    const bool vec = h_piece == 16 && w_piece == 16 && (g.E & 3) == 0;
     const int whole = (int)(d / kRouteDepth);
     const char* h_src = reinterpret_cast<const char*>(hrow) + (threadIdx.x & 7) * 16;
     const char* w_src = reinterpret_cast<const char*>(Wr) + threadIdx.x * 16;
@@ -598,27 +601,29 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
                 if ((int)threadIdx.x * 16 + j * (kRouteThreads * 16) < w_chunk)
                     cp_async<16>(w_at[j] + so, src + j * (kRouteThreads * 16), 16);
         } else if (c < chunks) {
+            // pieces in the order they lie; what is past the last column reads as zero
             const int64_t k0 = (int64_t)c * kRouteDepth;
             const int cols = (int)(d - k0 < kRouteDepth ? d - k0 : kRouteDepth);
             if (row_in) {
-                const int per = h_piece / (int)sizeof(H);
+                const int there = cols * (int)sizeof(H);
+                const char* src = reinterpret_cast<const char*>(hrow + k0);
 #pragma unroll 1
-                for (int k = (threadIdx.x & 7) * per; k < kRouteDepth; k += 8 * per) {
-                    const int left = (cols - k) * (int)sizeof(H);
-                    const int valid = left <= 0 ? 0 : left < h_piece ? left : h_piece;
-                    const H* src = hrow + k0 + (left > 0 ? k : 0);
-                    const uint32_t dst = h_dst + so + (uint32_t)k * (uint32_t)sizeof(H);
-                    if (h_piece == 16) cp_async<16>(dst, src, valid); else cp_async<8>(dst, src, valid);
+                for (int at = (threadIdx.x & 7) * h_piece; at < kRouteDepth * (int)sizeof(H); at += 8 * h_piece) {
+                    const int valid = at >= there ? 0 : there - at < h_piece ? there - at : h_piece;
+                    const char* from = src + (valid > 0 ? at : 0);
+                    if (h_piece == 16) cp_async<16>(h_dst + so + at, from, valid);
+                    else cp_async<8>(h_dst + so + at, from, valid);
                 }
             }
-            const float* src = Wr + k0 * g.E;
-            const int n = vec ? g.E >> 2 : g.E, floats = vec ? 4 : 1;   // pieces a row
+            const char* src = reinterpret_cast<const char*>(Wr + k0 * g.E);
+            const int there = cols * g.E * 4, per_row = g.E >> 2;
 #pragma unroll 1
-            for (int i = threadIdx.x; i < kRouteDepth * n; i += kRouteThreads) {
-                const int k = i / n, e = i - k * n;
-                const uint32_t dst = w_dst + so + k * w_row + e * floats * 4;
-                const float* from = src + (k < cols ? i * floats : 0);
-                if (vec) cp_async<16>(dst, from, k < cols ? 16 : 0); else cp_async<4>(dst, from, k < cols ? 4 : 0);
+            for (int i = threadIdx.x; i * w_piece < w_chunk; i += kRouteThreads) {
+                const int at = i * w_piece;
+                const int valid = at >= there ? 0 : there - at < w_piece ? there - at : w_piece;
+                const uint32_t dst = w_dst + so + (padded ? (i / per_row) * w_row + (i % per_row) * 16u : (uint32_t)at);
+                const char* from = src + (valid > 0 ? at : 0);
+                if (w_piece == 16) cp_async<16>(dst, from, valid); else cp_async<4>(dst, from, valid);
             }
         }
         cp_async_commit();
@@ -818,11 +823,48 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     // experts of a row, 32 rows a warp: 32.5 us instead of 30.2 at T = 4096 4096 x 16, 57.2
     // instead of 53.6 at T = 777 5120 x 64.)
     constexpr int kCols = 16, kRows = kRouteThreads / 2;
-    double* sums = reinterpret_cast<double*>(smem);   // [8 warps][2]
+    double* sums = reinterpret_cast<double*>(smem);   // [8 warps][2], or one a thread
     const int which = threadIdx.x & 1, row0 = (int)threadIdx.x >> 1, w_step = kRows * g.E;
 #pragma unroll 1
     for (int u = q; u < ntok; u += C) {
         uint64_t rest = open_s[u];
+        // many at once (all, where a softmax score with a bias is open): a thread an
+        // expert, whole rows of Wr.  Both ways' time, in tenths of a microsecond (T =
+        // 777 4096 x 64, softmax and bias: 108 us, two at a time 345; T = 616 648 x 64:
+        // 17 and 59).
+        if (__popcll(rest) * (5 + 4 * (int)((d + 2047) >> 11)) > 7 * (int)((d * EMAX + 4095) >> 12)) {
+            constexpr int kStep = kRouteThreads / EMAX;   // rows at a time
+            const int e = threadIdx.x % EMAX, r0 = threadIdx.x / EMAX;
+            const H* px = h + (tok0 + u) * ldh + r0;
+            const float* pw = Wr + (int64_t)r0 * g.E + (e < g.E ? e : 0);
+            double v = 0.0;
+#pragma unroll 1
+            for (int left = (int)((d - r0 + kStep - 1) / kStep); left > 0; left -= kCols) {
+                float x[kCols], w[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    x[c] = w[c] = 0.f;
+                    if (c < left) {
+                        x[c] = route_load(px + c * kStep);
+                        w[c] = __ldg(pw);
+                    }
+                    pw += kStep * g.E;
+                }
+                px += kCols * kStep;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) v = fma((double)x[c], (double)w[c], v);
+            }
+            sums[threadIdx.x] = v;
+            __syncthreads();
+            if ((int)threadIdx.x < g.E) {
+                double t = 0.0;
+#pragma unroll 1
+                for (int r = 0; r < kStep; ++r) t += sums[r * EMAX + threadIdx.x];
+                fixed[u * kMaxExperts + threadIdx.x] = t;
+            }
+            __syncthreads();
+            continue;
+        }
 #pragma unroll 1
         while (rest != 0) {
             const int ea = __ffsll((long long)rest) - 1;
