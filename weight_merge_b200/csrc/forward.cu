@@ -241,7 +241,7 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
     for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
         L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
         L.vsteps = 0;
-        e = launch_down(L, ctx, s, &L.busy);
+        e = launch_down(L, ctx, s, &L);
         L.vsteps = L.terms * L.bsteps;
         if (e == cudaSuccess) e = launch_product(L, ctx, s);
     }

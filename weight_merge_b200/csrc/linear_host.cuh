@@ -248,6 +248,14 @@ inline int pair_width(int64_t tok_tiles, int rows, int64_t pairs, int nsteps, do
     return best;
 }
 
+// SMs for a product's CTA pairs: beside a launch before it that holds a quarter of
+// them or fewer, those it leaves (T = 333, 4096 -> 4096, 4 experts of rank 4: 22.9 us
+// on 62 pairs; on 74, of which 12 wait 9 us for their SMs, 29.0); otherwise all (T =
+// 765, 1120 -> 14312 fp32, 16 experts of rank 16: 47 us; beside 72 CTAs 68).
+inline int64_t pair_count(const TcLinear& L, const adafuse_ctx* ctx) {
+    return (ctx->sm_count - (L.busy <= ctx->sm_count / 4 ? L.busy : 0)) / 2;
+}
+
 // More than 128 tokens: the skinny kernel (tiles of 128 x 128, contraction
 // split) where its estimate is below the pair kernel's, that is where the pair
 // kernel has too few tiles to occupy the SMs.  Measured at T = 333 4096 -> 1024:
@@ -255,7 +263,7 @@ inline int pair_width(int64_t tok_tiles, int rows, int64_t pairs, int nsteps, do
 inline bool pair_is_faster(const TcLinear& L, const adafuse_ctx* ctx) {
     const int nsteps = L.xsteps + L.vsteps, sm_count = ctx->sm_count;
     double pair_us;
-    pair_width(ceil_div(L.p.T, kPairTokens), L.rows, (sm_count - L.busy) / 2, nsteps, &pair_us);
+    pair_width(ceil_div(L.p.T, kPairTokens), L.rows, pair_count(L, ctx), nsteps, &pair_us);
     const int64_t tiles = ceil_div(L.rows, L.tile_rows) * ceil_div(L.p.T, 128);
     const int S = skinny_split(tiles, nsteps, L.busy, cluster_room(ctx));
     const double skinny_us = 7.0 + (double)(ceil_div(tiles * S, sm_count) * ceil_div(nsteps, S)) * 0.19;
@@ -266,7 +274,7 @@ inline bool pair_is_faster(const TcLinear& L, const adafuse_ctx* ctx) {
 template <bool F32, int MODE>
 cudaError_t launch_pair(TcLinear L, const uint16_t* W, const adafuse_ctx* ctx, cudaStream_t s) {
     L.tok_tiles = (int)ceil_div(L.p.T, kPairTokens);
-    const int64_t most = (ctx->sm_count - L.busy) / 2;
+    const int64_t most = pair_count(L, ctx);
     double us;
     const int BN = pair_width(L.tok_tiles, L.rows, most, L.xsteps + L.vsteps, &us);
     CUtensorMap map_w, map_x, map_b, map_v;
@@ -299,24 +307,24 @@ inline cudaError_t launch_product(TcLinear L, const adafuse_ctx* ctx, cudaStream
     return launch_skinny_any<kProduct>(L, map_w, map_b, ctx, s, &ctas);
 }
 
-// V of a routed product.  Returns in *busy the CTAs that the product launched
-// next leaves their SMs: this launch's where they are few, so that the product
-// runs beside them (where they are many, it starts as they end).
-inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s, int* busy) {
+// V of a routed product.  Notes in *next the SMs that this launch holds, up to
+// half of them: the product launched next is laid out to run beside it (beside a
+// larger launch nothing would be left: it starts as that one ends).
+inline cudaError_t launch_down(TcLinear L, const adafuse_ctx* ctx, cudaStream_t s, TcLinear* next) {
     CUtensorMap map_a, none;
     std::memset(&none, 0, sizeof none);
     L.rows = L.p.E * L.p.r;
     L.tile_rows = 128 / L.p.r * L.p.r;
     L.xsteps = (int)ceil_div(L.p.in, 64);
     L.vsteps = L.busy = 0;
-    *busy = 0;
+    next->busy = 0;
     if (L.p.T > 128 && L.rp == L.p.r && pair_is_faster(L, ctx))
         return L.terms == 2 ? launch_pair<true, kDown>(L, L.p.A, ctx, s)
                             : launch_pair<false, kDown>(L, L.p.A, ctx, s);
     if (!encode_rows(&map_a, L.p.A, L.rows, L.p.in, L.p.in, 128)) return cudaErrorInvalidValue;
     int ctas = 0;
     const cudaError_t e = launch_skinny_any<kDown>(L, map_a, none, ctx, s, &ctas);
-    if (ctas <= ctx->sm_count / 4) *busy = ctas;
+    if (ctas <= ctx->sm_count / 2) next->busy = ctas;
     return e;
 }
 

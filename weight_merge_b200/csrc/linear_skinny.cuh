@@ -84,11 +84,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return true;
 }
 
-__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -511,29 +506,42 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
                 r8 = e * L.p.r + k;
             }
             if (r8 < nrow) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                // (kDown: reads past an expert's or the tile's last row stay inside the
+                // ring and are left out later; rows that start anywhere are read as
+                // the three aligned vectors around them: T = 371, 8376 -> 288, 16 experts
+                // of rank 21 42 us, read one by one 60)
                 const uint32_t off = part_s + (uint32_t)(tok * 128 + r8) * 4u;
+                const bool anywhere = MODE == kDown && (L.p.r & 3) != 0;
+                const uint32_t from = anywhere ? off & ~15u : off;
+                float v[MODE == kDown ? 12 : 8];
+#pragma unroll
+                for (int i = 0; i < (MODE == kDown ? 12 : 8); ++i) v[i] = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < S; ++c) {
-                    uint32_t a = off;
-                    if (S > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(off), "r"(c));
-                    if (MODE == kDown && (L.p.r & 7) != 0) {
-                        // an expert's rows start anywhere; reads past the tile's
-                        // last row stay inside the ring and are left out later
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += ld_cluster_f1(a + 4u * i);
-                    } else {
-                        const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
-                        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-                        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                    uint32_t a = from;
+                    if (S > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(from), "r"(c));
+                    const float4 lo = ld_cluster_f4(a), hi = ld_cluster_f4(a + 16);
+                    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+                    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+                    if constexpr (MODE == kDown) {
+                        if (anywhere) {
+                            const float4 end = ld_cluster_f4(a + 32);
+                            v[8] += end.x; v[9] += end.y; v[10] += end.z; v[11] += end.w;
+                        }
                     }
                 }
-                if constexpr (MODE == kDown)
-                    finish_down8(L, tok0 + tok, row0 / L.p.r + e, k, v, bad);
-                else
+                if constexpr (MODE == kDown) {
+                    const uint32_t sh = (off >> 2 & 3u);
+                    if (anywhere) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = sh < 2 ? (sh == 0 ? v[i] : v[i + 1]) : (sh == 2 ? v[i + 2] : v[i + 3]);
+                    }
+                    const float u[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+                    finish_down8(L, tok0 + tok, row0 / L.p.r + e, k, u, bad);
+                } else {
                     finish_cols(L.p, tok0 + tok, row0 + r8, v, side);
+                }
             }
             request(gi + kSkinnyThreads);
         }
