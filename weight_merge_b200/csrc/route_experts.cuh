@@ -21,6 +21,14 @@
 // each of C CTAs), then runs, 8 warps and the CTAs, so with
 // m = 40 + kRouteRun + n / kRouteRun + 1 + 8 + C
 //   |z - z64| <= m 2^-24 sum |h w| <= m 2^-24 |h| |w|   (Cauchy-Schwarz).
+// |h| and |w| come from fp32 sums of squares, which say nothing where the squares
+// underflow: a sum with any nonzero value in it is kept above zero, so that 0
+// means a row (or a router) of zeros, whose logits are exact; below kRouteTiny
+// nothing is bounded and every logit is open.  Above it |h| and |w| are at least
+// 2^-40, and what terms below the normal range 2^-126 lose is no more than
+//   in a sum of squares     d 2^-126                     (2^-15 of it for any d);
+//   in splitting h and w    2^-126 sqrt(d) (|h| + |w|)   (2^-45 |h| |w| 2^-24);
+//   in products and sums    2^-126 each, 16 a column     (d 2^-122).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -39,6 +47,7 @@ struct GateParams {
 };
 
 constexpr int kMaxExperts = 64;
+constexpr float kRouteTiny = 0x1p-80f;   // of a sum of squares, see the file's head
 
 __device__ __forceinline__ double warp_max(double v) {
 #pragma unroll
@@ -505,21 +514,21 @@ __device__ __forceinline__ void route_mma(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A token tile's 16 columns as A fragments, one plane per term, and the squares
-// of its values added to the lane's two rows.
-__device__ __forceinline__ void route_h_frag(const float* r0, const float* r1, uint32_t (&a)[3][4], float& s0,
-                                             float& s1) {
+// A token tile's 16 columns as A fragments, one plane per term; the squares of
+// its values added to the lane's two rows, their bits to the rows' (s, b).
+__device__ __forceinline__ void route_h_frag(const float* r0, const float* r1, uint32_t (&a)[3][4], float (&s)[2],
+                                             uint32_t (&b)[2]) {
     const float2 v[4] = {*reinterpret_cast<const float2*>(r0), *reinterpret_cast<const float2*>(r1),
                          *reinterpret_cast<const float2*>(r0 + 8), *reinterpret_cast<const float2*>(r1 + 8)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         split3(v[i].x, v[i].y, a[0][i], a[1][i], a[2][i]);
-        float& s = i & 1 ? s1 : s0;
-        s = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, s));
+        s[i & 1] = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, s[i & 1]));
+        b[i & 1] |= __float_as_uint(v[i].x) | __float_as_uint(v[i].y);
     }
 }
 __device__ __forceinline__ void route_h_frag(const __nv_bfloat16* r0, const __nv_bfloat16* r1,
-                                             uint32_t (&a)[1][4], float& s0, float& s1) {
+                                             uint32_t (&a)[1][4], float (&s)[2], uint32_t (&b)[2]) {
     a[0][0] = *reinterpret_cast<const uint32_t*>(r0);
     a[0][1] = *reinterpret_cast<const uint32_t*>(r1);
     a[0][2] = *reinterpret_cast<const uint32_t*>(r0 + 8);
@@ -527,9 +536,15 @@ __device__ __forceinline__ void route_h_frag(const __nv_bfloat16* r0, const __nv
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float x = __uint_as_float(a[0][i] << 16), y = __uint_as_float(a[0][i] & 0xffff0000u);
-        float& s = i & 1 ? s1 : s0;
-        s = fmaf(x, x, fmaf(y, y, s));
+        s[i & 1] = fmaf(x, x, fmaf(y, y, s[i & 1]));
     }
+    b[0] |= a[0][0] | a[0][2];
+    b[1] |= a[0][1] | a[0][3];
+}
+// A sum of squares above zero wherever one of its values is (bits: theirs, all
+// taken together; `signs` are left out).
+__device__ __forceinline__ float keep_nonzero(float s, uint32_t bits, uint32_t signs) {
+    return (bits & ~signs) != 0 && s < FLT_MIN ? FLT_MIN : s;
 }
 // h may come from the launch before, under whose end this one is set up: it is
 // no constant data.
@@ -644,6 +659,19 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) ww[n] = 0.f;
     int in_run = 0;
+    uint32_t w_bits = 0, h_bits[2][2] = {{0, 0}, {0, 0}};
+    // what fragment reads past the last expert meet, row padding and slack, is zero
+    {
+        const uint32_t per = padded ? w_row - (uint32_t)g.E * 4u : 0u;   // 0 or 16 bytes a row
+        const uint32_t tail = (uint32_t)kRouteDepth * w_row;
+        for (int s = 0; s < kRouteStages; ++s) {
+            uint8_t* w = smem + (size_t)s * stage_bytes + kRouteTokens * kPitch;
+            if (per != 0 && threadIdx.x < kRouteDepth)
+                *reinterpret_cast<uint4*>(w + threadIdx.x * w_row + g.E * 4) = make_uint4(0u, 0u, 0u, 0u);
+            if (threadIdx.x >= kRouteThreads - 64)
+                *reinterpret_cast<uint32_t*>(w + tail + (threadIdx.x - (kRouteThreads - 64)) * 4) = 0u;
+        }
+    }
 
     sm100::pdl_wait();   // set-up overlaps the end of the launch before this one
     sm100::pdl_launch_dependents();
@@ -663,13 +691,15 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
         for (int m = 0; m < 2; ++m) {
             const H* r0 = reinterpret_cast<const H*>(base + (size_t)(16 * m + g8) * kPitch) + 16 * warp + 2 * tig;
             const H* r1 = reinterpret_cast<const H*>(reinterpret_cast<const uint8_t*>(r0) + 8 * kPitch);
-            route_h_frag(r0, r1, a[m], hh[m][0], hh[m][1]);
+            route_h_frag(r0, r1, a[m], hh[m], h_bits[m]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float* w = wt + 8 * n;
             const float w0 = w[0], w1 = w[w_pitch], w2 = w[8 * w_pitch], w3 = w[9 * w_pitch];
             ww[n] = fmaf(w0, w0, fmaf(w1, w1, fmaf(w2, w2, fmaf(w3, w3, ww[n]))));
+            w_bits |= __float_as_uint(w0) | __float_as_uint(w1);
+            w_bits |= __float_as_uint(w2) | __float_as_uint(w3);
             uint32_t b[3][2];
             split3(w0, w1, b[0][0], b[1][0], b[2][0]);
             split3(w2, w3, b[0][1], b[1][1], b[2][1]);
@@ -702,6 +732,12 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
         }
         if (++stage == kRouteStages) stage = 0;
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ww[n] = keep_nonzero(ww[n], w_bits, 0x80000000u);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        hh[m >> 1][m & 1] = keep_nonzero(hh[m >> 1][m & 1], h_bits[m >> 1][m & 1],
+                                         sizeof(H) == 2 ? 0x80008000u : 0x80000000u);
     cp_async_wait<0>();
     __syncthreads();   // the ring is free
 
@@ -796,12 +832,15 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
         float z[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) z[i] = sub + LPT * i < g.E ? zrow[sub + LPT * i] : 0.f;
-        // 1.02: the squares are fp32 sums themselves; terms below fp32's normal
-        // range are off by up to 2^-149 each instead.  (A NaN in Wr shows in z.)
-        // A router of zeros (as they are initialised) is exact.
-        const float delta = wmax == 0.f ? 0.f
-                                        : 1.02f * roundings * 0x1p-24f * sqrtf(zrow[EMAX]) * sqrtf(wmax) +
-                                              (float)d * 0x1p-148f;
+        // the squares are sums of fp32 themselves: 4 additions a chunk, and 1.02 for
+        // joining them and for what underflows.  (A NaN in Wr shows in z.)
+        const float hh = zrow[EMAX];
+        float delta = INFINITY;   // every logit is open
+        if (hh == 0.f || wmax == 0.f)
+            delta = 0.f;
+        else if (hh >= kRouteTiny && wmax >= kRouteTiny)
+            delta = (1.02f + (float)mine_chunks * 0x1p-22f) * roundings * 0x1p-24f * sqrtf(hh) * sqrtf(wmax) +
+                    (float)d * 0x1p-122f;
         const uint64_t open = route_decide32<LPT, EPL>(z, delta, g, sub, lane - sub, valid, ends + slot * 4 * EMAX,
                                                        route, tok0 + t);
         if (valid) {
