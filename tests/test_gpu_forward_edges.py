@@ -70,3 +70,83 @@ def test_route_rows_and_columns_of_any_magnitude_together():
     route_check(sw, h, Wr, 8, score="softmax", k=8)
     Wr[:, :] *= 2.0 ** -70
     route_check(sw, h, Wr, 8, score="softmax", k=8)
+
+
+ZERO_ROWS = [
+    # T, d, E, score, k, groups, top, group_top, bias
+    (1, 64, 8, "softmax", 2, 1, 1, 1, None), (1, 64, 64, "sigmoid", 8, 8, 3, 2, "equal"),
+    (40, 512, 8, "softmax", 2, 4, 2, 1, None), (70, 512, 16, "sigmoid", 4, 4, 2, 2, "random"),
+    (70, 516, 16, "softmax", 3, 1, 1, 1, "equal"), (300, 1028, 64, "softmax", 8, 8, 3, 1, None),
+    (300, 256, 64, "sigmoid", 8, 8, 4, 2, "few"), (2500, 64, 12, "softmax", 6, 3, 2, 2, "few"),
+    (4600, 64, 24, "sigmoid", 4, 2, 1, 2, "few"),
+]
+
+
+@pytest.mark.parametrize("T,d,E,score,k,G,top,gt,bias", ZERO_ROWS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_route_rows_of_zeros(T, d, E, score, k, G, top, gt, bias, dtype):
+    """Padded rows of a batch: every logit 0 (of either sign), picks by bias, group
+    and index."""
+    _, sw = model(8, 8, E=E)
+    g = gen(T + E)
+    h = rows(g, T, d, dtype, pad=8)
+    Wr = torch.randn((d, E), generator=g, device="cuda") * 0.05
+    b = None
+    if bias is not None:
+        b = torch.randn((E,), generator=g, device="cuda")
+        b = torch.full_like(b, 0.25) if bias == "equal" else b.round() if bias == "few" else b
+    kw = dict(score=score, k=k, n_groups=G, top_groups=top, group_top=gt, bias=b)
+    some = torch.rand((T,), generator=g, device="cuda") < 0.5
+    h[some] = 0.0
+    h[some, ::3] = -0.0
+    route_check(sw, h, Wr, 8, **kw)
+    route_check(sw, h, torch.zeros_like(Wr), 8, **kw)
+    # 0 * inf and 0 * nan are no logits; a row of zeros but for one is none of zeros
+    h[0] = 0.0
+    h[T // 2, d - 1] = 2.0 ** -100
+    route_check(sw, h, Wr, 8, **kw)
+    Wr[d // 2, E // 2] = float("inf")
+    with np.errstate(invalid="ignore"):
+        idx, _ = route_check(sw, h, Wr, 8, **kw)
+    assert np.all(idx[0] == -1)
+
+
+def device_us(fn, n=25):
+    """The median device time of a call, with the host ahead."""
+    for _ in range(3):
+        fn()
+    took = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda._sleep(100000)
+        a.record()
+        fn()
+        b.record()
+        torch.cuda.synchronize()
+        took.append(a.elapsed_time(b) * 1e3)
+    return sorted(took)[n // 2]
+
+
+@pytest.mark.parametrize("T,d,E,k,G,bias", [(2048, 4096, 8, 2, 1, False), (777, 4096, 64, 8, 8, False),
+                                            (1024, 4096, 16, 4, 4, True), (64, 4096, 8, 2, 1, False)])
+def test_route_rows_of_zeros_cost_no_more(T, d, E, k, G, bias):
+    """A padded batch takes as long as a full one: where each row of zeros was
+    summed in fp64, these took four to eight times as long."""
+    _, sw = model(8, 8, E=E)
+    g = gen(1)
+    h = rows(g, T, d, F32).contiguous()
+    Wr = torch.randn((d, E), generator=g, device="cuda") * 0.05
+    gating = Bnd.make_gating(k=k, n_groups=G, top_groups=max(G // 2, 1),
+                             bias=torch.zeros((E,), device="cuda") if bias else None)
+    slots = 2 if k <= 2 else 4 if k <= 4 else 8
+    rt = torch.zeros((T, 2 * slots), dtype=torch.int32, device="cuda")
+
+    def us(x, w):
+        return device_us(lambda: sw.route_experts(x, w, gating, rt, stream()))
+
+    full = us(h, Wr)
+    last, every = h.clone(), h.clone()
+    last[T // 2:] = 0
+    every[::2] = 0
+    for x, w in ((last, Wr), (every, Wr), (torch.zeros_like(h), Wr), (h, torch.zeros_like(Wr))):
+        assert us(x, w) < 1.5 * full

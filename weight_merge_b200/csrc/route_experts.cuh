@@ -63,18 +63,26 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// One token's decision by one warp, in 64 bits.  Lane l holds the logits of
-// experts l (z0) and l + 32 (z1); scratch: kMaxExperts doubles of shared memory
-// that belong to this warp.  Writes the record at route[t].
+// One decision by one warp, in 64 bits.  Lane l holds the logits of experts l
+// (z0) and l + 32 (z1); scratch: kMaxExperts doubles of shared memory that belong
+// to this warp.  Writes the record of every token in `tokens` (bit i: i-th record
+// from `route` on), whose logits these are.
 __device__ __noinline__ void route_decide64(double z0, double z1, const GateParams g, int lane, double* scratch,
-                                            int32_t* __restrict__ route, int64_t t) {
+                                            int32_t* __restrict__ route, uint32_t tokens) {
     const double kNone = -INFINITY;
     const bool in0 = lane < g.E, in1 = lane + 32 < g.E;
-    int32_t* idx_out = route + t * 2 * g.slots;
-    float* gate_out = reinterpret_cast<float*>(idx_out + g.slots);
+    auto write = [&](int idx, float gate) {
+        for (uint32_t rest = tokens; rest != 0; rest &= rest - 1) {
+            int32_t* rec = route + (__ffs((int)rest) - 1) * 2 * g.slots;
+            if (lane < g.slots) {
+                rec[lane] = idx;
+                reinterpret_cast<float*>(rec)[g.slots + lane] = gate;
+            }
+        }
+    };
     const bool fine = (!in0 || fabs(z0) <= (double)FLT_MAX) && (!in1 || fabs(z1) <= (double)FLT_MAX);
     if (!__all_sync(0xffffffffu, fine)) {
-        if (lane < g.slots) { idx_out[lane] = -1; gate_out[lane] = 0.f; }
+        write(-1, 0.f);
         return;
     }
     // scores: softmax over all E, or sigmoid (exp overflows to +inf for very
@@ -183,10 +191,7 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
                     : expf((float)(fmin(my_z, 0.0) - fmin(zmax, 0.0))) / (1.f + expf((float)-fabs(my_z)));
         gate = x / warp_sum((double)x);
     }
-    if (lane < g.slots) {
-        idx_out[lane] = lane < n ? my_pick : -1;
-        gate_out[lane] = lane < n ? (float)(gate * (double)g.scale) : 0.f;
-    }
+    write(lane < n ? my_pick : -1, lane < n ? (float)(gate * (double)g.scale) : 0.f);
 }
 
 // The same decision in 32 bits, LPT lanes a token and EPL <= 2 experts a lane:
@@ -738,6 +743,8 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     for (int m = 0; m < 4; ++m)
         hh[m >> 1][m & 1] = keep_nonzero(hh[m >> 1][m & 1], h_bits[m >> 1][m & 1],
                                          sizeof(H) == 2 ? 0x80008000u : 0x80000000u);
+    __shared__ uint32_t zeros_s;   // tokens whose logits are all 0 and whose ties the fp64 decision settles
+    if (threadIdx.x == 0) zeros_s = 0;
     cp_async_wait<0>();
     __syncthreads();   // the ring is free
 
@@ -813,7 +820,7 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
 
     // ---- decisions: CTA q takes tokens q, q + C, ...
     constexpr int LPT = route_lanes<EMAX>(), EPL = EMAX / LPT;
-    __shared__ uint64_t open_s[kRouteTokens];
+    __shared__ uint64_t open_s[kRouteTokens];   // logits to be summed in fp64
     const int sub = lane % LPT, slot = (int)threadIdx.x / LPT;
     float wmax = 0.f;
 #pragma unroll
@@ -841,9 +848,21 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
         else if (hh >= kRouteTiny && wmax >= kRouteTiny)
             delta = (1.02f + (float)mine_chunks * 0x1p-22f) * roundings * 0x1p-24f * sqrtf(hh) * sqrtf(wmax) +
                     (float)d * 0x1p-122f;
-        const uint64_t open = route_decide32<LPT, EPL>(z, delta, g, sub, lane - sub, valid, ends + slot * 4 * EMAX,
-                                                       route, tok0 + t);
+        uint64_t open = route_decide32<LPT, EPL>(z, delta, g, sub, lane - sub, valid, ends + slot * 4 * EMAX,
+                                                 route, tok0 + t);
+        // A row (or a router) of zeros has nothing to sum: its logits are 0 as they
+        // stand, and all such tokens share one decision.
+        bool nonzero = delta != 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) nonzero = nonzero || z[i] != 0.f;   // a NaN is
+        const uint32_t seg = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1) << (lane - sub);
+        const bool zeros = (__ballot_sync(0xffffffffu, nonzero) & seg) == 0;
         if (valid) {
+            if (zeros && open != 0) {
+                if (sub == 0) atomicOr(&zeros_s, 1u << t);
+                some_open = true;
+                open = 0;
+            }
             if (sub == 0) open_s[t] = open;
             if (open != 0) {
                 some_open = true;
@@ -947,7 +966,11 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
     for (int u = q + C * warp; u < ntok; u += C * kRouteWarps)
         if (open_s[u] != 0)
             route_decide64(fixed[u * kMaxExperts + lane], fixed[u * kMaxExperts + 32 + lane], g, lane,
-                           fixed + (kRouteTokens + warp) * kMaxExperts, route, tok0 + u);
+                           fixed + (kRouteTokens + warp) * kMaxExperts, route + tok0 * 2 * g.slots, 1u << u);
+    // (by the warp that has the fewest of them)
+    if (warp == kRouteWarps - 1 && zeros_s != 0)
+        route_decide64(0.0, 0.0, g, lane, fixed + (kRouteTokens + warp) * kMaxExperts, route + tok0 * 2 * g.slots,
+                       zeros_s);
 }
 
 }  // namespace adafuse
