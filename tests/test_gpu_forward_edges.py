@@ -150,3 +150,64 @@ def test_route_rows_of_zeros_cost_no_more(T, d, E, k, G, bias):
     every[::2] = 0
     for x, w in ((last, Wr), (every, Wr), (torch.zeros_like(h), Wr), (h, torch.zeros_like(Wr))):
         assert us(x, w) < 1.5 * full
+
+
+# --------------------------------------------------------------------------
+# the product with its epilogue
+
+def act_exact(v, name):
+    """The activation in 64 bits, in forms that do not cancel, and how far 32
+    bits may be from it, relative to it, in units of u = 2^-24.
+
+    gelu = v h below 0, v (1 - h) above, h = t p(t) e^w with w = -v^2 / 2: w is off
+    by 3u |w| (square, constant, product), e^w by as much and 2 ulp (4u); t by 3u
+    (sum, 2 ulp of its inverse), p by 1.5e-7 (2.5u) and 2u of its evaluation, three
+    products: 1.5 v^2 + 15, and 1 for 1 - h.  gelu_tanh = v / (1 + e^w): w off by
+    4u |w| (square, two constants or their sum, product), e^w by as much and 2 ulp
+    (4u), the sum 1u, the division 2 ulp (4u).  silu the same with w = -v exact and a
+    rounded division."""
+    if name == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / np.sqrt(2.0)), 1.5 * v * v + 16
+    if name == "gelu_tanh":
+        w = -2 * np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3)
+        return v / (1 + torch.exp(w)), 4 * w.abs() + 9
+    if name == "silu":
+        return v / (1 + torch.exp(-v)), torch.full_like(v, 4 + 2)
+    return torch.where(v < 0, 0.0, v), torch.zeros_like(v)
+
+
+@pytest.mark.parametrize("T,inn,out", [(1, 64, 1024), (8, 64, 1024), (40, 128, 1032), (300, 128, 520), (700, 64, 2056)])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_activations_keep_their_digits_far_below_zero(T, inn, out, act):
+    """Arguments that the product gives exactly (each row of x picks a column of
+    W), from -8 to 8, the result times a large factor."""
+    m, sw = model(out, inn, E=1, r=8)
+    g = gen(T)
+    m.W[0].copy_((torch.rand((out, inn), generator=g, device="cuda") * 16 - 8).to(BF))
+    pick = torch.randint(0, inn, (T,), generator=g, device="cuda")
+    x = torch.zeros((T, inn), dtype=BF, device="cuda")
+    x[torch.arange(T, device="cuda"), pick] = 1.0
+    mul = torch.randn((T, out), generator=g, device="cuda") * 1e6
+    v = m.W[0].double().t()[pick]
+    for factor in (None, mul):
+        y = torch.empty((T, out), dtype=F32, device="cuda")
+        sw.linear(0, 0, x, y, activation=ACT[act], mul=factor, stream=stream())
+        torch.cuda.synchronize()
+        want, units = act_exact(v, act)
+        if factor is not None:
+            want, units = want * factor.double(), units + 1
+        check(y, want.cpu(), (units * 2.0 ** -24 * want.abs() + 1e-37).cpu())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_activations_of_huge_arguments(T, act):
+    inf, nan, top = float("inf"), float("nan"), 3.4e38
+    bias = torch.tensor([inf, nan, 1e30, -1e30, top, -top, 100.0, -300.0], device="cuda")
+    m, sw = model(8, 64, E=1, r=8)
+    x = torch.zeros((T, 64), dtype=BF, device="cuda")
+    y = torch.empty((T, 8), dtype=F32, device="cuda")
+    sw.linear(0, 0, x, y, bias=bias, activation=ACT[act], stream=stream())
+    torch.cuda.synchronize()
+    want = torch.tensor([inf, nan, bias[2], 0.0, bias[4], 0.0, 100.0, 0.0], device="cuda")
+    assert torch.equal(y.nan_to_num(nan=-7.0, posinf=-8.0), want.nan_to_num(nan=-7.0, posinf=-8.0).expand(T, 8))

@@ -31,11 +31,31 @@ struct LinearParams {
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b) { return __uint_as_float(b << 16); }
 
+// GELU in forms that keep their digits where it is small: 1 + erf and 1 + tanh
+// cancel for negative v (three digits left at -4, none from -5.5 on).
+//
+// erf form: v (1 - h) for v >= 0 and v h below, h = erfc(|v| / sqrt 2) / 2.  h =
+// e^(-v^2 / 2) t p(t) with t = 1 / (1 + 0.3 |v|): h e^(v^2 / 2) falls like 1 / |v|,
+// so t takes [0, inf) to (0, 1] and p is smooth there.  p: least squares on the
+// relative error, reweighted until its peaks were level (1.5e-7; over |v| <= 14).
+// In all 1.5 v^2 + 16 units of 2^-24, most of it from rounding v^2.  (erfcf: T = 4096,
+// 4096 -> 14336 fp32 9% more time.)
 __device__ __forceinline__ float act_gelu(float v) {
-    return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    const float t = __fdividef(1.f, fmaf(0.3f, fabsf(v), 1.f));
+    float p = 0.0356770121f;
+    p = fmaf(p, t, -0.157212824f);
+    p = fmaf(p, t, 0.206370935f);
+    p = fmaf(p, t, -0.0537002124f);
+    p = fmaf(p, t, 0.128570631f);
+    p = fmaf(p, t, 0.0999106988f);
+    p = fmaf(p, t, 0.120754413f);
+    p = fmaf(p, t, 0.119629271f);
+    const float h = p * t * exp2f(v * v * -0.721347520f);
+    return v * (v < 0.f ? h : 1.f - h);
 }
+// tanh form: v / (1 + e^w), w = -2 sqrt(2 / pi) (v + 0.044715 v^3).
 __device__ __forceinline__ float act_gelu_tanh(float v) {
-    return 0.5f * v * (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+    return __fdividef(v, 1.f + exp2f(v * fmaf(v * v, -0.102943240f, -2.30220820f)));
 }
 __device__ __forceinline__ float act_silu(float v) { return v / (1.f + expf(-v)); }
 
