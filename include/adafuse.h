@@ -578,7 +578,8 @@ typedef struct adafuse_linear_args {
  * ADAFUSE_WEIGHT_BASE without a registered base; UNSUPPORTED_SHAPE for T
  * above 2^31 - 1.  One launch on `stream` per 2^17 tokens.  The tensor-core
  * kernels bound every wait; a launch whose wait runs out (1 s) raises
- * ADAFUSE_STATUS_TIMEOUT and leaves y incomplete. */
+ * ADAFUSE_STATUS_TIMEOUT and leaves y incomplete: every element holds its
+ * result or what was there before. */
 ADAFUSE_API int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stream);
 
 /* Bytes of device workspace adafuse_linear_routed needs for T tokens on this
@@ -603,10 +604,21 @@ ADAFUSE_API int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, 
  * workspace: 256-byte aligned device memory of at least
  * adafuse_linear_workspace bytes (INVALID_ARG otherwise); calls that may
  * overlap on the GPU need workspaces of their own.  Its contents before and
- * after the call mean nothing. */
+ * after the call mean nothing.
+ * A call of more than 8 tokens is two launches (per 2^17 tokens): x A^T, then the
+ * product.  The second stores nothing where it finds ADAFUSE_STATUS_TIMEOUT in
+ * the status word, raised by the first or left there by an earlier call. */
 ADAFUSE_API int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args,
                                       const void* routes, int32_t slots, void* workspace,
                                       int64_t workspace_bytes, void* stream);
+
+/* Test hook for the products' timeout path.  The `launch`-th (1-based)
+ * tensor-core launch of the next adafuse_linear or adafuse_linear_routed call of
+ * more than 8 tokens (per 2^17 tokens: the product, or x A^T and then the
+ * product) waits, in its first CTA or CTA pair, for an operand stage that never
+ * fills, so that the bounded wait runs out.  INVALID_ARG when launch < 1.
+ * Host-only; consumed by that call. */
+ADAFUSE_API int adafuse_debug_stall_next_product(adafuse_ctx* ctx, int32_t launch);
 
 /* Tile edge of the segment table (128). */
 ADAFUSE_API int adafuse_tile_size(void);

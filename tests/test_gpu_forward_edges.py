@@ -211,3 +211,83 @@ def test_activations_of_huge_arguments(T, act):
     torch.cuda.synchronize()
     want = torch.tensor([inf, nan, bias[2], 0.0, bias[4], 0.0, 100.0, 0.0], device="cuda")
     assert torch.equal(y.nan_to_num(nan=-7.0, posinf=-8.0), want.nan_to_num(nan=-7.0, posinf=-8.0).expand(T, 8))
+
+
+# --------------------------------------------------------------------------
+# launches that give up
+
+def held(y, want, tol):
+    """y's elements that are as they were (7); the others must be right."""
+    old = (y == 7.0).cpu()
+    check(torch.where(old, want.to(y.dtype), y.cpu()), want, tol)
+    return old
+
+
+STALLED = [
+    # T, in, out: clusters of CTAs that share a tile, single CTAs, CTA pairs
+    (40, 4096, 256, BF), (100, 2048, 1032, F32), (90, 136, 20000, BF), (600, 1024, 8192, F32), (1500, 520, 4096, BF),
+]
+
+
+@pytest.mark.parametrize("T,inn,out,dtype", STALLED)
+def test_a_product_that_gives_up_stores_only_finished_values(T, inn, out, dtype):
+    """The hook keeps the first CTA (pair) waiting until its bound (1 s): its
+    tile stays as it was, the other tiles hold the product, and the next call is
+    right everywhere."""
+    m, sw = model(out, inn, E=4, r=8, seed=T)
+    x = rows(gen(T), T, inn)
+    want, tol = ref.product(x, m.W[0], out_dtype=dtype)
+    y = torch.full((T, out), 7.0, dtype=dtype, device="cuda")
+    Bnd.adafuse_debug_stall_next_product(sw.ctx, 1)
+    sw.linear(0, 0, x, y, stream=stream())
+    assert sw.status(stream()) == Bnd.ADAFUSE_STATUS_TIMEOUT
+    old = held(y, want, tol)
+    assert old[0, 0] and not old[-1, -1]
+    sw.linear(0, 0, x, y, stream=stream())
+    assert sw.status(stream()) == 0
+    check(y, want, tol)
+
+
+@pytest.mark.parametrize("T,inn,out,dtype", STALLED)
+@pytest.mark.parametrize("launch", [1, 2])
+def test_a_routed_product_that_gives_up_stores_only_finished_values(T, inn, out, dtype, launch):
+    """The same in either launch of a routed product: what the second one would
+    make of an incomplete x A^T is not stored either."""
+    E, r = 16, 32
+    m, sw = model(out, inn, E=E, r=r, seed=T)
+    g = gen(T)
+    x, rt = rows(g, T, inn), make_routes(g, T, E, 2, 2)
+    want, tol = ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0, out_dtype=dtype)
+    y = torch.full((T, out), 7.0, dtype=dtype, device="cuda")
+    ws = workspace(sw, T, dtype == F32)
+    Bnd.adafuse_debug_stall_next_product(sw.ctx, launch)
+    sw.linear_routed(0, 0, x, rt, y, ws, stream=stream())
+    assert sw.status(stream()) == Bnd.ADAFUSE_STATUS_TIMEOUT
+    old = held(y, want, tol)
+    assert old.all() if launch == 1 else old[0, 0] and not old[-1, -1]
+    sw.linear_routed(0, 0, x, rt, y, ws, stream=stream())
+    assert sw.status(stream()) == 0
+    check(y, want, tol)
+
+
+def test_a_timeout_that_nobody_read_stops_the_next_routed_product():
+    T, inn, out, E = 40, 512, 256, 4
+    m, sw = model(out, inn, E=E, r=8)
+    g = gen(1)
+    x, rt = rows(g, T, inn), make_routes(g, T, E, 2, 2)
+    y = torch.full((T, out), 7.0, dtype=BF, device="cuda")
+    ws = workspace(sw, T, False)
+    Bnd.adafuse_debug_stall_next_product(sw.ctx, 1)
+    sw.linear(0, 0, x, torch.empty_like(y), stream=stream())
+    sw.linear_routed(0, 0, x, rt, y, ws, stream=stream())
+    assert sw.status(stream()) == Bnd.ADAFUSE_STATUS_TIMEOUT
+    assert (y == 7.0).all()
+    sw.linear_routed(0, 0, x, rt, y, ws, stream=stream())
+    assert sw.status(stream()) == 0
+    check(y, *ref.product(x, m.W[0], routes=rt, slots=2, A=m.A[0], B=m.B[0], s=2.0))
+
+
+def test_the_product_hook_refuses_a_launch_number_below_one():
+    _, sw = model(64, 64)
+    with pytest.raises(Bnd.AdafuseError):
+        Bnd.adafuse_debug_stall_next_product(sw.ctx, 0)

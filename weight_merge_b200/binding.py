@@ -147,6 +147,7 @@ def lib() -> ctypes.CDLL:
         "adafuse_rebase_topk": ([P, P, P], ctypes.c_int),
         "adafuse_debug_stall_next_switch": ([P], ctypes.c_int),
         "adafuse_debug_stall_next_switch_at": ([P, i32], ctypes.c_int),
+        "adafuse_debug_stall_next_product": ([P, i32], ctypes.c_int),
         "adafuse_refresh_adapters": ([P, P], ctypes.c_int),
         "adafuse_route_experts": ([P, P, i32, i64, i64, i64, P, ctypes.POINTER(Gating), i32, P, P],
                                   ctypes.c_int),
@@ -297,6 +298,11 @@ def adafuse_debug_stall_next_switch(ctx: int) -> None:
 def adafuse_debug_stall_next_switch_at(ctx: int, tile: int) -> None:
     _check(lib().adafuse_debug_stall_next_switch_at(ctx, int(tile)),
            "adafuse_debug_stall_next_switch_at")
+
+
+def adafuse_debug_stall_next_product(ctx: int, launch: int) -> None:
+    _check(lib().adafuse_debug_stall_next_product(ctx, int(launch)),
+           "adafuse_debug_stall_next_product")
 
 
 def adafuse_set_switch_kernel(ctx: int, kernel: int) -> None:

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <vector>
@@ -30,6 +31,7 @@ struct adafuse_ctx {
     CUtensorMap* d_w0_maps = nullptr;  // 1 per pair on the re-base source W0
     bool has_base = false;
     int stall_at = 0;  // test hook: the next tensor-core launch stalls at each CTA's n-th tile
+    std::atomic<int> stall_product{0};  // test hook: the n-th launch of the next product stalls
     // pair kernel: 256 x 128 blocks, layer-major like the tile table
     adafuse::TileEntry* d_blocks = nullptr;
     uint16_t* d_bpad = nullptr;              // rank < 8: B with rows zero-padded to 8

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -93,6 +94,11 @@ int linear_params(const adafuse_ctx* ctx, const adafuse_linear_args* a, LinearPa
     return ADAFUSE_OK;
 }
 
+// The pending request of the test hook: which launch of this call stalls, 0 = none.
+int take_stall(adafuse_ctx* ctx) {
+    return ctx->stall_product.load(std::memory_order_relaxed) == 0 ? 0 : ctx->stall_product.exchange(0);
+}
+
 // One launch of the router: 32 tokens a CTA, their columns shared by a cluster
 // of up to 8 CTAs while that keeps the grid resident at once (T = 1 4096 x 8, T =
 // 4096 4096 x 16, T = 777 5120 x 64: 5.8, 30.6, 53.7 us; on one CTA a group 19, 39,
@@ -174,8 +180,10 @@ int adafuse_linear(adafuse_ctx* ctx, const adafuse_linear_args* args, void* stre
     } else {
         TcLinear L;
         std::memset(&L, 0, sizeof L);
+        int stall = take_stall(ctx);
         for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
             L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
+            L.stall = --stall == 0;
             e = launch_product(L, ctx, s);
         }
     }
@@ -238,14 +246,23 @@ int adafuse_linear_routed(adafuse_ctx* ctx, const adafuse_linear_args* args, con
         p.B = padded;
     }
     L.bsteps = (int)ceil_div((int64_t)p.E * lay.rp, 64);
+    int stall = take_stall(ctx);
     for (int64_t t = 0; t < p.T && e == cudaSuccess; t += kTokensPerLaunch) {
         L.p = token_range(p, t, std::min(p.T - t, kTokensPerLaunch));
         L.vsteps = 0;
+        L.stall = --stall == 0;
         e = launch_down(L, ctx, s, &L);
         L.vsteps = L.terms * L.bsteps;
+        L.stall = --stall == 0;
         if (e == cudaSuccess) e = launch_product(L, ctx, s);
     }
     return e == cudaSuccess ? ADAFUSE_OK : cuda_fail(e, "routed linear launch");
+}
+
+int adafuse_debug_stall_next_product(adafuse_ctx* ctx, int32_t launch) {
+    if (ctx == nullptr || launch < 1) return ADAFUSE_ERR_INVALID_ARG;
+    ctx->stall_product = launch;
+    return ADAFUSE_OK;
 }
 
 }  // extern "C"

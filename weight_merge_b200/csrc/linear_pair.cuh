@@ -90,7 +90,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(&full[i], 4);     // one arrival, with its bytes, from each loading warp
+            // one arrival, with its bytes, from each loading warp
+            mbar_init(&full[i], i == 0 && L.stall && blockIdx.x == 0 ? 5 : 4);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -277,6 +278,9 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
             } else {
                 src = await_chunk();
             }
+            // V has landed, so the launch that wrote it is complete: did it give up?
+            if (MODE == kProduct && ok && t == t_first && L.vsteps > 0)
+                ok = (status_now(L.p) & ADAFUSE_STATUS_TIMEOUT) == 0;
             if (!ok) { fail(); break; }
 #pragma unroll 1
             for (int cb = group; cb < blocks; cb += 4) {

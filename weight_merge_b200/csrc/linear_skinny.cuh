@@ -50,6 +50,7 @@ struct TcLinear {
     int tile_rows;     // rows of a tile that are its own: 128, or whole experts of kDown
     int tok_tiles;     // token tiles
     int busy;          // SMs that the launch before holds (host only)
+    int stall;         // test hook: the first CTA's (pair's) first stage never fills
 };
 
 constexpr int kSkinnyThreads = 384;
@@ -89,6 +90,19 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// The context's status word as it is now.
+__device__ __forceinline__ int status_now(const LinearParams& p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p.status) : "memory");
     return v;
 }
 
@@ -323,7 +337,8 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(&full[i], 2);     // one arrival, with its bytes, from each loading warp
+            // one arrival, with its bytes, from each loading warp
+            mbar_init(&full[i], i == 0 && L.stall && blockIdx.x == 0 ? 3 : 2);
             mbar_init(&empty[i], 1);
         }
         mbar_init(acc_full, 1);
@@ -469,9 +484,13 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
             }
         }
         if (ok) {
+            // V has landed, so the launch that wrote it is complete: did it give up?
+            int down = 0;
+            if (MODE == kProduct && L.vsteps > 0 && threadIdx.x == 0) down = status_now(L.p);
 #pragma unroll
             for (int i = 0; i < kCols; ++i) part[(half + i) * 128 + (warp & 3) * 32 + lane] = sum[i];
             tc_fence_before();
+            if (down & ADAFUSE_STATUS_TIMEOUT) *abort_flag = 1;
         } else {
             fail();
         }
@@ -492,8 +511,14 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
     };
     request(g0 + (int)threadIdx.x);
     __syncthreads();
-    if (S > 1) cluster_sync();
-    if (!*abort_flag) {
+    // where any CTA of the cluster gave up there is no tile to store
+    bool whole = !*abort_flag;
+    if (S > 1) {
+        cluster_sync();
+        const uint32_t gave_up = lane < S ? ld_cluster_u32(cluster_addr((const void*)abort_flag, (uint32_t)lane)) : 0u;
+        whole = !__any_sync(0xffffffffu, gave_up != 0);
+    }
+    if (whole) {
         const uint32_t part_s = smem_u32(part);
         int bad = 0;
 #pragma unroll 1
