@@ -32,6 +32,11 @@ def test_structs_have_the_c_layout():
     assert Bnd._pack_linear_args(*fields) == bytes(Bnd.LinearArgs(*fields))
 
 
+def test_a_gating_built_directly_keeps_no_tensor():
+    assert Bnd.Gating(0, 2, 1, 1, 1, 1, 1.0, None)._keep is None
+    assert Bnd.make_gating(k=3)._keep is None
+
+
 def test_route_by_hand():
     # logits 2, 1, 0, 3 for one token
     h = torch.tensor([[1.0, 0.0]])

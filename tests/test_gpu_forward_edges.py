@@ -72,6 +72,22 @@ def test_route_rows_and_columns_of_any_magnitude_together():
     route_check(sw, h, Wr, 8, score="softmax", k=8)
 
 
+def test_route_with_a_gating_built_directly():
+    T, d, E = 20, 64, 8
+    _, sw = model(8, 8, E=E)
+    g = gen(2)
+    h, Wr = rows(g, T, d, F32), torch.randn((d, E), generator=g, device="cuda")
+    b = torch.randn((E,), generator=g, device="cuda")
+    for bias in (None, b):
+        made = Bnd.make_gating(score=SCORE["sigmoid"], k=2, n_groups=2, bias=bias)
+        direct = Bnd.Gating(SCORE["sigmoid"], 2, 2, 1, 1, 1, 1.0, None if bias is None else bias.data_ptr())
+        got = [torch.zeros((T, 4), dtype=torch.int32, device="cuda") for _ in range(2)]
+        sw.route_experts(h, Wr, made, got[0], stream())
+        sw.route_experts(h, Wr, direct, got[1], stream())
+        torch.cuda.synchronize()
+        assert torch.equal(*got)
+
+
 ZERO_ROWS = [
     # T, d, E, score, k, groups, top, group_top, bias
     (1, 64, 8, "softmax", 2, 1, 1, 1, None), (1, 64, 64, "sigmoid", 8, 8, 3, 2, "equal"),

@@ -74,6 +74,9 @@ class Route8(ctypes.Structure):
 
 
 class Gating(ctypes.Structure):
+    """adafuse_gating.  Built directly, ``bias`` is a device address (or None) that
+    the caller answers for; make_gating takes a tensor, checks and keeps it."""
+    _keep = None   # the bias tensor, where make_gating was given one
     _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
