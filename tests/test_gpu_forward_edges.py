@@ -307,3 +307,62 @@ def test_the_product_hook_refuses_a_launch_number_below_one():
     _, sw = model(64, 64)
     with pytest.raises(Bnd.AdafuseError):
         Bnd.adafuse_debug_stall_next_product(sw.ctx, 0)
+
+
+# --------------------------------------------------------------------------
+# long sums
+
+LONG = [
+    # T, in, out: W streamed past the tensor cores; clusters and single CTAs whose
+    # accumulators are emptied; CTA pairs, one and several tiles each
+    (1, 11008, 512), (8, 14336, 1024), (61, 11008, 4096), (100, 11008, 11008), (128, 14336, 14336),
+    (128, 8192, 19200), (700, 11008, 2048), (2048, 11008, 4096), (2050, 14336, 1032),
+]
+
+
+def one_sided(g, n, k):
+    """Values of one sign: every partial sum grows, so each step's loss shows."""
+    return (torch.rand((n, k), generator=g, device="cuda") + 0.5).to(BF)
+
+
+@pytest.mark.parametrize("T,inn,out", LONG)
+@pytest.mark.parametrize("signs", ["mixed", "one"])
+@pytest.mark.parametrize("routed", [False, True])
+def test_fp32_outputs_of_long_sums(T, inn, out, signs, routed):
+    """The relative norm of the error of fp32 outputs over long contractions.
+
+    A tensor-core accumulator cuts what a 16-deep piece adds below its last bit:
+    on average half a unit of 2^-23 of itself, a piece; n pieces on one lose
+    n / 2 units of a sum that grows evenly to its end, half of that of the end's
+    value: n 2^-25.  With 48 pieces at most 48 / 2^25 = 1.4e-6 if every sum grows
+    evenly (signs of one kind), and its square root's share of it if they wander;
+    2^-24 sqrt(20) = 2.7e-7 for the fp32 additions that join up to 20 parts, and
+    2^-24 for the rest: 1.8e-6.  One chain of 688 pieces would leave 2e-5 (one sign).
+    Mixed signs: sums that wander are on average 2/3 of their end, 0.95e-6: 1.3e-6.
+    V as two bf16 terms: each within 2^-18 of its value, independently: 2^-18 of
+    the adapters' part."""
+    E, r = 4, 8
+    m, sw = model(out, inn, E=E, r=r, seed=T)
+    g = gen(inn + T)
+    x = rows(g, T, inn).contiguous()
+    if signs == "one":
+        x = one_sided(g, T, inn)
+        m.W[0].copy_(one_sided(g, out, inn))
+    y = torch.empty((T, out), dtype=F32, device="cuda")
+    xd = x.double()
+    want = xd @ m.W[0].double().t()
+    tol = (1.8e-6 if signs == "one" else 1.3e-6) * want.norm()
+    if routed:
+        rt = make_routes(g, T, E, 2, 2)
+        gates = ref.dense_gates(rt, 2, E).cuda()
+        part = torch.zeros_like(want)
+        for e in range(E):
+            part += (2.0 * gates[:, e:e + 1] * (xd @ m.A[0][e].double().t())) @ m.B[0][e].double().t()
+        want += part
+        tol += (2.0 ** -18 + 1.8e-6) * part.norm()
+        sw.linear_routed(0, 0, x, rt, y, workspace(sw, T, True), stream=stream())
+    else:
+        sw.linear(0, 0, x, y, stream=stream())
+    torch.cuda.synchronize()
+    off = (y.double() - want).norm()
+    assert off <= tol, (off / want.norm()).item()
