@@ -366,3 +366,58 @@ def test_fp32_outputs_of_long_sums(T, inn, out, signs, routed):
     torch.cuda.synchronize()
     off = (y.double() - want).norm()
     assert off <= tol, (off / want.norm()).item()
+
+
+# --------------------------------------------------------------------------
+# operands that the call before wrote
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_every_operand_may_come_from_the_call_before(T):
+    """Bias, router, balance bias, weight and adapters made by a product right
+    before the call that reads them, in one graph without a gap, over buffers
+    that held something else before."""
+    n, E, r = 256, 8, 16
+    src, made = model(n, n, E=E, r=r, seed=5)                  # makes the operands
+    g = gen(T)
+    W, A, B = (torch.zeros(s, dtype=BF, device="cuda") for s in ((n, n), (E, r, n), (E, n, r)))
+    sw = Bnd.Switcher([W], [A], [B], 1, 1, E, r, 2.0 * r, device=torch.cuda.current_device())
+    shapes = {"bias": (1, n), "W": (n, n), "A": (E * r, n), "Bt": (E * n * r // n, n), "Wr": (n * E // n, n)}
+    seeds = {k: rows(g, v[0], n).contiguous() for k, v in shapes.items()}
+    x, h = rows(g, T, n), rows(g, T, n)
+    bias, bal = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    Wr = torch.zeros((n, E), device="cuda")
+    rt = make_routes(g, T, E, 2, 2)
+    rec = torch.zeros((T, 4), dtype=torch.int32, device="cuda")
+    ys = [torch.zeros((T, n), device="cuda") for _ in range(3)]
+    ws = workspace(sw, T, True)
+    gating = Bnd.make_gating(k=2, bias=bal[:E])
+    torch.cuda.synchronize()
+
+    def calls(s):
+        made.linear(0, 0, seeds["bias"], bias.view(1, n), stream=s)
+        sw.linear(0, 0, x, ys[0], bias=bias, stream=s)
+        made.linear(0, 0, seeds["W"], W, stream=s)
+        sw.linear(0, 0, x, ys[1], stream=s)
+        made.linear(0, 0, seeds["A"], A.view(-1, n), stream=s)
+        made.linear(0, 0, seeds["Bt"], B.view(-1, n), stream=s)
+        sw.linear_routed(0, 0, x, rt, ys[2], ws, stream=s)
+        made.linear(0, 0, seeds["Wr"], Wr.view(-1, n), stream=s)
+        made.linear(0, 0, seeds["bias"], bal.view(1, n), stream=s)
+        sw.route_experts(h, Wr, gating, rec, s)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        calls(torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        for k in seeds:
+            seeds[k].copy_(torch.randn(seeds[k].shape, generator=g, device="cuda"))
+        old_W = W.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(bias.view(1, n), *ref.product(seeds["bias"], src.W[0], out_dtype=F32))
+        check(W, *ref.product(seeds["W"], src.W[0]))
+        check(ys[0], *ref.product(x, old_W, bias=bias, out_dtype=F32))
+        check(ys[1], *ref.product(x, W, out_dtype=F32))
+        check(ys[2], *ref.product(x, W, routes=rt, slots=2, A=A, B=B, s=2.0, out_dtype=F32))
+        idx, _, _ = ref.route(h, Wr, score="softmax", k=2, bias=bal[:E])
+        assert np.array_equal(rec[:, :2].cpu().numpy(), idx)

@@ -87,7 +87,7 @@ __device__ __forceinline__ void apply_act(float (&v)[N], int act) {
 
 // One element of y: v is the finished product (bias not yet added).
 __device__ __forceinline__ void store_one(const LinearParams& p, int64_t t, int o, float v) {
-    if (p.bias != nullptr) v += __ldg(p.bias + o);
+    if (p.bias != nullptr) v += p.bias[o];
     float one[1] = {v};
     apply_act(one, p.act);
     v = one[0];
@@ -148,7 +148,7 @@ __device__ __forceinline__ void finish_cols(const LinearParams& p, int64_t t, in
     if (p.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (o + i < p.out) v[i] += __ldg(p.bias + o + i);
+            if (o + i < p.out) v[i] += p.bias[o + i];
     }
     apply_act(v, p.act);
     if (p.mul != nullptr) {
@@ -239,7 +239,7 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, int64_t tok0
     float bias[S::kCols];
     if (p.bias != nullptr && col < p.out) {
 #pragma unroll
-        for (int i = 0; i < S::kCols; ++i) bias[i] = __ldg(p.bias + col + i);
+        for (int i = 0; i < S::kCols; ++i) bias[i] = p.bias[col + i];
     }
     float w[S::kIters * S::kCols];
 #pragma unroll

@@ -588,14 +588,14 @@ linear_skinny_kernel(const __grid_constant__ TcLinear L, const __grid_constant__
 // Ranks above 8 that are not multiples of 8: B [E, out, r] copied to rows of
 // rp columns, zero past r (B rows of 2 * r bytes are no legal TMA stride).
 __global__ void __launch_bounds__(256)
-pad_b_kernel(const uint16_t* __restrict__ B, uint16_t* __restrict__ dst, int64_t nrows, int r, int rp) {
+pad_b_kernel(const uint16_t* B, uint16_t* dst, int64_t nrows, int r, int rp) {
     const int64_t total = nrows * rp;
     pdl_wait();   // the launch before may still read dst
     pdl_launch_dependents();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / rp;
         const int k = (int)(i % rp);
-        dst[i] = k < r ? __ldg(B + row * r + k) : (uint16_t)0;
+        dst[i] = k < r ? B[row * r + k] : (uint16_t)0;
     }
 }
 

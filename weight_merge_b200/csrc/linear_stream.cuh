@@ -9,9 +9,9 @@
 // sides, those and the same columns of one token's x are the A and B fragments
 // of four mma.m16n8k16 as they stand, so W goes from memory through registers
 // to the tensor cores.  A warp's next kStreamDepth steps, the next unit's
-// included, are requested as soon as the last ones are consumed.  x stays in L1
-// (plain loads: a launch set up while the one before it still writes must not read
-// its output as constant data).
+// included, are requested as soon as the last ones are consumed.  x stays in L1.
+// (Every operand comes by plain loads, in this file and the others: a launch set up
+// while the one before it still writes must not read its output as constant data.)
 //
 // Every sum is fp32; the partial sums of the warps and of the cluster's CTAs
 // are added in a fixed order.
@@ -49,17 +49,17 @@ __device__ __forceinline__ void ldg_stream16(const uint16_t* p, int n, uint32_t 
     for (int i = 0; i < 8; ++i) v[i] = 0u;
     if constexpr (WIDE) {
         if (n > 0)
-            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
                            "=r"(v[6]), "=r"(v[7])
                          : "l"(p));
     } else {
         if (n > 0)
-            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
+            asm volatile("ld.global.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "l"(p));
         if (n > 8)
-            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
+            asm volatile("ld.global.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                          : "l"(p + 8));
     }
@@ -93,7 +93,7 @@ __device__ __forceinline__ float adapters_of(const LinearParams& p, const Stream
         if ((p.r & 7) == 0) {
 #pragma unroll 1
             for (int k = 0; k < p.r; k += 8) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + k));
+                const uint4 w = *reinterpret_cast<const uint4*>(b + k);
                 const float4 u0 = __ldcg(reinterpret_cast<const float4*>(ue + k));
                 const float4 u1 = __ldcg(reinterpret_cast<const float4*>(ue + k + 4));
                 d = fmaf(__uint_as_float(w.x << 16), u0.x, d);
@@ -106,7 +106,7 @@ __device__ __forceinline__ float adapters_of(const LinearParams& p, const Stream
                 d = fmaf(__uint_as_float(w.w & 0xffff0000u), u1.w, d);
             }
         } else {
-            for (int k = 0; k < p.r; ++k) d = fmaf(bf16_bits_to_float(__ldg(b + k)), __ldcg(ue + k), d);
+            for (int k = 0; k < p.r; ++k) d = fmaf(bf16_bits_to_float(b[k]), __ldcg(ue + k), d);
         }
         v = fmaf(sl.g[t * p.slots + j], d, v);
     }

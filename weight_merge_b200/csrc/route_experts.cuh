@@ -49,6 +49,19 @@ struct GateParams {
 constexpr int kMaxExperts = 64;
 constexpr float kRouteTiny = 0x1p-80f;   // of a sum of squares, see the file's head
 
+// h, Wr and the bias may come from the launch before, under whose end this one is
+// set up: they are no constant data.
+__device__ __forceinline__ float route_load(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float route_load(const __nv_bfloat16* p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return __uint_as_float((uint32_t)v << 16);
+}
+
 __device__ __forceinline__ double warp_max(double v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -115,8 +128,8 @@ __device__ __noinline__ void route_decide64(double z0, double z1, const GatePara
     double q0 = s0, q1 = s1;            // selection values
     double key0 = z0, key1 = z1;        // what picks are ordered by
     if (g.bias != nullptr) {
-        if (in0) { const float b = __ldg(g.bias + lane); on0 = b > -INFINITY; q0 = s0 + (double)b; }
-        if (in1) { const float b = __ldg(g.bias + lane + 32); on1 = b > -INFINITY; q1 = s1 + (double)b; }
+        if (in0) { const float b = route_load(g.bias + lane); on0 = b > -INFINITY; q0 = s0 + (double)b; }
+        if (in1) { const float b = route_load(g.bias + lane + 32); on1 = b > -INFINITY; q1 = s1 + (double)b; }
         key0 = q0;
         key1 = q1;
     }
@@ -275,7 +288,7 @@ __device__ __forceinline__ uint64_t route_decide32(const float (&z)[EPL], float 
         q[i] = s[i];
         on[i] = false;
         if (in[i]) {
-            const float b = g.bias != nullptr ? __ldg(g.bias + sub + LPT * i) : 0.f;
+            const float b = g.bias != nullptr ? route_load(g.bias + sub + LPT * i) : 0.f;
             on[i] = b > -INFINITY;
             if (g.bias != nullptr) {
                 q[i] = s[i] + b;
@@ -551,19 +564,6 @@ __device__ __forceinline__ void route_h_frag(const __nv_bfloat16* r0, const __nv
 __device__ __forceinline__ float keep_nonzero(float s, uint32_t bits, uint32_t signs) {
     return (bits & ~signs) != 0 && s < FLT_MIN ? FLT_MIN : s;
 }
-// h may come from the launch before, under whose end this one is set up: it is
-// no constant data.
-__device__ __forceinline__ float route_load(const float* p) {
-    float v;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ float route_load(const __nv_bfloat16* p) {
-    uint16_t v;
-    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return __uint_as_float((uint32_t)v << 16);
-}
-
 // h_piece / w_piece: bytes of a copy (16, or 8 / 4 where rows or Wr are aligned
 // to no more).
 template <int EMAX, typename H>
@@ -904,7 +904,7 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
                     x[c] = w[c] = 0.f;
                     if (c < left) {
                         x[c] = route_load(px + c * kStep);
-                        w[c] = __ldg(pw);
+                        w[c] = route_load(pw);
                     }
                     pw += kStep * g.E;
                 }
@@ -942,7 +942,7 @@ route_experts_kernel(const H* __restrict__ h, const int64_t T, const int64_t d, 
                     x[c] = w[c] = 0.f;
                     if (c < left) {
                         x[c] = route_load(px + c * kRows);
-                        w[c] = __ldg(pw);
+                        w[c] = route_load(pw);
                     }
                     pw += w_step;
                 }
