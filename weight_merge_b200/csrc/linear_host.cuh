@@ -75,9 +75,12 @@ inline bool encode_b(CUtensorMap* m, const TcLinear& L, int nrow) {
     return encode_map(m, 4, L.p.B, dim, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Workspace of a routed product: V (or, for few tokens, u = x A^T in fp32: four
-// bytes a value cover either), then (ranks above 8 that are not
-// multiples of 8) the padded copy of B.
+// Workspace of a routed product: V (or, for up to kStreamMaxTokens tokens, u = x A^T
+// in fp32: four bytes a value cover either), then, where more tokens meet a rank above
+// 8 that is no multiple of 8, a padded copy of B.  That copy is made by each call:
+// B may change between calls, and a copy kept with the context (as for ranks below
+// 8, where it is at most 8 columns an expert) would hold up to twice the adapters'
+// memory for every weight.
 struct RoutedLayout {
     int rp, terms;
     bool pad;          // B is padded per call
@@ -91,7 +94,7 @@ inline RoutedLayout routed_layout(const adafuse_ctx* ctx, const PairDesc& pd, in
     w.pad = ctx->rank % 8 != 0 && pd.Bk == pd.B;
     w.v_bytes = round_up(T * ctx->n_experts * w.rp * 4, 256);
     w.bytes = w.v_bytes;
-    if (w.pad && T > 0) w.bytes += round_up((int64_t)ctx->n_experts * pd.out * w.rp * 2, 256);
+    if (w.pad && T > kStreamMaxTokens) w.bytes += round_up((int64_t)ctx->n_experts * pd.out * w.rp * 2, 256);
     return w;
 }
 
