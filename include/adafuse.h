@@ -55,7 +55,8 @@
  * a route) make the switch write NOTHING and raise a bit in the context's
  * device status word (read it with adafuse_get_device_status).  No C++
  * exception crosses this boundary.  A context may be used from one host
- * thread and one stream at a time.
+ * thread and one stream at a time (the per-token calls, below, from several
+ * at once).
  */
 #ifndef ADAFUSE_H_
 #define ADAFUSE_H_
@@ -264,8 +265,8 @@ ADAFUSE_API int adafuse_set_tile_schedule(adafuse_ctx* ctx, int schedule);
  * beside it; a caller that pipelines the switch against its forward pass
  * (adafuse_switch_batch_layers on a second stream) leaves SMs to the forward
  * this way.  The grid only decides which CTA takes a tile, never how a tile
- * is computed: W is bit for bit the same.  INVALID_ARG for max_ctas < 0.
- * Host-only, no device work. */
+ * is computed: W is bit for bit the same.  The per-token calls are not
+ * capped.  INVALID_ARG for max_ctas < 0.  Host-only, no device work. */
 ADAFUSE_API int adafuse_set_max_ctas(adafuse_ctx* ctx, int32_t max_ctas);
 
 /* The kernel adafuse_switch will launch (ADAFUSE_KERNEL_MMA_SYNC,
@@ -528,7 +529,8 @@ typedef struct adafuse_gating {
  * aligned, d and ldh multiples of 4, ldh >= d.  Wr: [d, E] fp32, 4-byte
  * aligned.  d below 2^31.  route: 16-byte aligned.  E comes from the context.
  * T == 0 is a no-op.  One launch on `stream`.  Tokens with equal or nearly
- * equal logits cost more (tens of microseconds a token where all 64 tie). */
+ * equal logits cost more (tens of microseconds a token where all 64 tie), and
+ * so do rows of h or a Wr whose norm is below 2^-40; rows of zeros do not. */
 ADAFUSE_API int adafuse_route_experts(adafuse_ctx* ctx, const void* h, int32_t h_dtype, int64_t T,
                                       int64_t d, int64_t ldh, const float* Wr,
                                       const adafuse_gating* gating, int32_t slots, void* route,
@@ -594,9 +596,10 @@ ADAFUSE_API int adafuse_linear_workspace(const adafuse_ctx* ctx, int32_t layer, 
  * adafuse_route_experts; 16-byte aligned).  The same expert in two slots
  * counts with the sum of its gates.  A slot whose index is outside [-1, E) or
  * whose gate is not finite raises ADAFUSE_STATUS_BAD_EXPERT / _BAD_GATE and
- * counts as empty.  x A_e^T is accumulated in fp32; for ADAFUSE_DTYPE_BF16
- * outputs its gated values may be carried as bf16, for ADAFUSE_DTYPE_F32 as
- * two bf16 terms (relative 2^-17).  W is not changed.  A and B hold finite
+ * counts as empty.  x A_e^T is accumulated in fp32.  Up to 8 tokens its gated
+ * values stay fp32; above, they are carried as bf16 for ADAFUSE_DTYPE_BF16
+ * outputs and as two bf16 terms (relative 2^-17) for ADAFUSE_DTYPE_F32, so a
+ * token's result may differ in its last bits with the number of tokens.  W is not changed.  A and B hold finite
  * values: an infinity or NaN in an expert's B may reach tokens that did not
  * choose it (x may hold anything: a token's row affects that token only).  For
  * ranks below 8 B is read as the switches read it: adafuse_refresh_adapters

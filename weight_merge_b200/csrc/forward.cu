@@ -101,7 +101,7 @@ int take_stall(adafuse_ctx* ctx) {
 
 // One launch of the router: 32 tokens a CTA, their columns shared by a cluster
 // of up to 8 CTAs while that keeps the grid resident at once (T = 1 4096 x 8, T =
-// 4096 4096 x 16, T = 777 5120 x 64: 5.8, 30.6, 53.7 us; on one CTA a group 19, 39,
+// 4096 4096 x 16, T = 777 5120 x 64: 6.1, 31.4, 54.1 us; on one CTA a group 19, 39,
 // 145).
 template <int EMAX, typename H>
 cudaError_t launch_route_as(const H* h, int64_t T, int64_t d, int64_t ldh, const float* Wr, const GateParams& g,

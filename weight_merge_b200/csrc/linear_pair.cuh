@@ -12,12 +12,13 @@
 // multiple of 16): the host takes the width whose tiles fill whole rounds.
 //
 // F32 (fp32 outputs, V of two terms): tensor-core accumulators drop low bits on
-// every 16-deep piece (1e-6 of the result after 64, more in proportion), so the
-// contraction is cut into chunks of at most kChunkSteps steps, each started from
-// zero, and the epilogue adds them in registers in fp32.  7e-7 of the result is
-// left; chunks of 24 steps left 1.4e-6 and took 301 instead of 308 us for T =
-// 4096, 11008 -> 4096 with 8 experts of rank 8.  A bf16 output does not see the
-// difference and takes one chunk.
+// every 16-deep piece (1e-6 of the result after 64, more in proportion; 4e-6 where
+// all products have one sign), so the contraction is cut into chunks of at most
+// kChunkSteps steps, each started from zero, and the epilogue adds them in
+// registers in fp32.  7e-7 of the result is left; chunks of 24 steps left 1.4e-6
+// and took 301 instead of 308 us for T = 4096, 11008 -> 4096 with 8 experts of rank
+// 8.  A bf16 output, rounded at 2^-9 of itself, takes one chunk: at 4096 columns one
+// in 400 values is rounded the other way, and the error's norm stays 0.00166.
 //
 // Routed products: after x and W come V and the stacked B, as in
 // linear_skinny.cuh; kDown writes V (F32: as two terms).
@@ -243,7 +244,8 @@ linear_pair_kernel(const __grid_constant__ TcLinear L, const __grid_constant__ C
                 // The chunks' sums in registers; with the last chunk they go
                 // back to TMEM, from where the loop below takes them.  (Held in
                 // registers through that loop they would spill, and with the
-                // ring in shared memory L1 is too small for spills.)
+                // ring in shared memory L1 is too small for more than the 16
+                // bytes a thread that are spilled as it is.)
                 float acc[4][16];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

@@ -38,7 +38,7 @@ constexpr int kStreamRows = 16;
 // on the tensor-core kernel for more tokens 20.0 and 19.5.
 constexpr int kStreamMaxTokens = 8;
 // Steps in flight per warp, 2 KB each (T = 1, 4096 -> 11008: 16.8, 16.2 and 24.8 us
-// for one, two and three, which spill).
+// for one, two and three, which spill 0, 12 and 112 bytes a thread there).
 constexpr int kStreamDepth = 2;
 
 // 16 consecutive bf16 of a row (n = 16, 8 or 0 of them inside it), read past L1.
